@@ -81,7 +81,8 @@ typedef enum pbs_status {
 } pbs_status;
 
 enum { PBS_OP_PERMUTE = 0, PBS_OP_SELECT = 1, PBS_OP_ATTN = 2, PBS_OP_PERMUTE_SEGMENTED = 3,
-       PBS_OP_SELECT_SEGMENTED = 4, PBS_OP_SELECT_SAMPLE = 5, PBS_OP_PERMUTE_QUERIES = 6 };
+       PBS_OP_SELECT_SEGMENTED = 4, PBS_OP_SELECT_SAMPLE = 5, PBS_OP_PERMUTE_QUERIES = 6,
+       PBS_OP_ATTN_WINDOW = 7, PBS_OP_ATTN_PREFIX = 8, PBS_OP_KEY_MASS = 9, PBS_OP_EVICT = 10 };
 enum { PBS_SELECT_TOPK = 0, PBS_SELECT_TAU = 1, PBS_SELECT_SAMPLE = 2 };
 /* OR-ed into pbs_select's mode: write lists in visiting order, and/or read
  * one permutation per query segment (see there). */
@@ -90,7 +91,10 @@ enum { PBS_SELECT_SCORE_ORDER = 0x10, PBS_SELECT_PERM_PER_SEGMENT = 0x20 };
 enum { PBS_ATTN_EARLY_STOP = 1, PBS_ATTN_PERM_PER_SEGMENT = 2, PBS_ATTN_CTA_PAIR = 4 };
 
 /* Bytes of workspace the given op needs for these shapes (0 if none).
- * Q and K may not be NULL; only their shapes are read.                     */
+ * Q and K may not be NULL; only their shapes are read.  The cache
+ * operators (PBS_OP_ATTN_WINDOW and after) do not read blk and seg; for
+ * PBS_OP_ATTN_PREFIX K is the sequences' own cache, and for PBS_OP_EVICT Q
+ * is not read (pass K twice).                                              */
 size_t pbs_workspace_size(int op, const pbs_tensor* Q, const pbs_tensor* K,
                           int blk, int seg);
 
@@ -305,6 +309,98 @@ int pbs_attn_fwd_ex(const pbs_tensor* Q, const pbs_tensor* K, const pbs_tensor* 
                     const int32_t* counts, const int32_t* idx, int cap, int blk, int seg, unsigned flags,
                     const float* gate_thr, float stop_tau, float softmax_scale, pbs_tensor* O, float* lse,
                     long long* stats, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Cache operators: attention over the K/V cache that a prefill leaves, and
+ * keeping that cache short.  They share these conventions.
+ *
+ *  - K and V are caches [B, Hkv, N, D] with room for N keys, of which the
+ *    first kv_len[b] are filled (kv_len: DEVICE int32 [B], or NULL: all N).
+ *    Whatever lies at and after kv_len[b] is never read into a result.
+ *  - Q [B, Hq, M, D] holds the newest M tokens of each sequence, or with
+ *    q_len (DEVICE int32 [B], or NULL: all M) the newest q_len[b], in its
+ *    first q_len[b] rows.  Row r stands at key position
+ *        pos = kv_len[b] - q_len[b] + r,
+ *    so one new token is M = 1, a whole prompt M = N, and a batch of prompts
+ *    of unequal length is padded at the end.  Rows at and after q_len[b] are
+ *    not computed: their outputs are left as they were.
+ *  - Lengths outside [0, N] or [0, M] are clamped and set the device error
+ *    word (PBS_ERR_DEVICE_CHECK).
+ *  - Key j is visible to a row at pos if j <= pos and, with window > 0,
+ *    j > pos - window or j < n_sink: a sliding window of the last `window`
+ *    keys (the row's own included) and n_sink first keys that stay visible.
+ *    window = 0: every key up to pos.
+ *  - A row that sees no key gives O = 0 and lse = -inf.
+ *  - M and N are any positive lengths (no multiple of a block); Hq / Hkv is
+ *    at most 64.  K and V may be broadcast views (zero batch or head
+ *    strides); Q and O may not.  Hkv * B is at most 65535.
+ *  - What a row sees decides its result: NaN or infinity in a key, or in the
+ *    value of a key, that the row does not see leaves it unchanged.
+ *  - Two calls that may overlap in time need two workspaces, also where they
+ *    are captured into graphs.                                               */
+
+/* pbs_attn_window: O = softmax(softmax_scale * Q K^T) V over the visible
+ * keys (scaled-dot-product attention with a sliding window and sinks).
+ *   window: >= 0; n_sink: >= 0; softmax_scale: positive and finite.
+ *   O: bf16 [B, Hq, M, D]; lse: NULL or DEVICE fp32 [B, Hq, M], natural-log
+ *   normaliser of the scaled logits.
+ *   ws: pbs_workspace_size(PBS_OP_ATTN_WINDOW, Q, K, ...) bytes.            */
+int pbs_attn_window(const pbs_tensor* Q, const pbs_tensor* K, const pbs_tensor* V, const int32_t* kv_len,
+                    const int32_t* q_len, int64_t window, int n_sink, float softmax_scale, pbs_tensor* O, float* lse,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* pbs_attn_prefix: attention of a batch whose sequences share a prefix.  Kp
+ * and Vp are the prefix's cache [1, Hkv, P, D], held once; K and V hold each
+ * sequence's own keys after it.  A row sees all P prefix keys and the keys
+ * j <= pos of its own cache, pos as above (a row with pos < 0 sees the prefix
+ * alone).  The prefix is read once for the whole batch.  Other arguments as
+ * for pbs_attn_window; ws: pbs_workspace_size(PBS_OP_ATTN_PREFIX, Q, K, ...)
+ * bytes.                                                                     */
+int pbs_attn_prefix(const pbs_tensor* Q, const pbs_tensor* Kp, const pbs_tensor* Vp, const pbs_tensor* K,
+                    const pbs_tensor* V, const int32_t* kv_len, const int32_t* q_len, float softmax_scale,
+                    pbs_tensor* O, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* pbs_key_mass: the attention weight that each key receives, added to what
+ * it has received before:
+ *   mass[b,hkv,j] = decay * prev[b,hkv,j]
+ *                 + sum over the query heads h of KV head hkv and the rows r
+ *                   that see j of exp(softmax_scale * Q[b,h,r].K[b,hkv,j]
+ *                                     - lse[b,h,r])
+ * for j < kv_len[b], and 0 for the others (a key appended later starts at
+ * zero).
+ *   lse: DEVICE fp32 [B, Hq, M], from whichever attention ran over these
+ *     queries and keys; a row with lse = -inf adds nothing.
+ *   prev, mass: DEVICE fp32 [B, Hkv, N], successive (b, hkv) rows
+ *     prev_stride / mass_stride elements apart (>= N).  prev may be NULL (no
+ *     earlier mass; decay is not used) or the same buffer as mass.
+ *   decay: finite, >= 0.
+ *   ws: pbs_workspace_size(PBS_OP_KEY_MASS, Q, K, ...) bytes.
+ * The sums have a fixed order: equal inputs give equal bits.                */
+int pbs_key_mass(const pbs_tensor* Q, const pbs_tensor* K, const float* lse, const int32_t* kv_len,
+                 const int32_t* q_len, int64_t window, int n_sink, float decay, float softmax_scale,
+                 const float* prev, int64_t prev_stride, float* mass, int64_t mass_stride, void* ws, size_t ws_bytes,
+                 void* stream);
+
+/* pbs_evict: shortens every cache to `budget` keys by accumulated mass.  Of
+ * the kv_len[b] keys of (b, hkv) it keeps the first n_sink, the last
+ * `recent`, and of the others those of highest mass up to budget in all
+ * (ties to the lower position; -0 equals 0; NaN ranks lowest).  With
+ * kv_len[b] <= budget every key stays.
+ *   mass: DEVICE fp32 [B, Hkv, N], rows mass_stride elements apart.
+ *   budget in [1, N], n_sink + recent <= budget.
+ *   keep: DEVICE int32 [B, Hkv, budget], the kept positions in ascending
+ *     order, -1 after the last.
+ *   new_len: DEVICE int32 [B], min(kv_len[b], budget); NULL if not wanted.
+ *   K_out, V_out: bf16 [B, Hkv, N_out, D] with N_out >= budget, the kept rows
+ *     in that order; mass_out: DEVICE fp32, rows mass_out_stride (>= budget)
+ *     elements apart, their mass.  Rows at and after new_len[b] are left as
+ *     they were.  None of them may overlap K, V or mass; K_out and V_out may
+ *     not be broadcast views.
+ *   ws: pbs_workspace_size(PBS_OP_EVICT, K, K, ...) bytes.                  */
+int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* K, const pbs_tensor* V,
+              const int32_t* kv_len, int budget, int recent, int n_sink, int32_t* keep, int32_t* new_len,
+              pbs_tensor* K_out, pbs_tensor* V_out, float* mass_out, int64_t mass_out_stride, void* ws,
+              size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then returns and clears the sticky device error
  * word of the current device (PBS_OK if no device-side check failed).      */

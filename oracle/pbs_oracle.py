@@ -764,3 +764,94 @@ def dense_lists(B: int, Hq: int, nb: int, blk: int, seg: int) -> Tuple[np.ndarra
                 lists[(b, h, i)] = arr
                 counts[b, h, i] = arr.size
     return counts, lists
+
+
+# --------------------------------------------------------------------------
+# cache operators: attention over a K/V cache and keeping it short
+# --------------------------------------------------------------------------
+def visible_keys(pos: int, window: int, n_sink: int) -> np.ndarray:
+    """Ascending keys that a row at key position ``pos`` sees: those up to
+    ``pos`` that lie within the last ``window`` (0: all) or among the first
+    ``n_sink``."""
+    if pos < 0:
+        return np.zeros(0, np.int64)
+    first = 0 if window == 0 else max(0, pos - window + 1)
+    return np.concatenate([np.arange(min(n_sink, first)), np.arange(first, pos + 1)]).astype(np.int64)
+
+
+def _cache_rows(B: int, M: int, N: int, kv_len, q_len):
+    """(b, row, key position) of every query row that is computed."""
+    for b in range(B):
+        L = N if kv_len is None else int(kv_len[b])
+        n = M if q_len is None else int(q_len[b])
+        for r in range(n):
+            yield b, r, L - n + r
+
+
+def attn_cache(Q, K, V, window: int = 0, n_sink: int = 0, kv_len=None, q_len=None, scale: Optional[float] = None,
+               Kp=None, Vp=None):
+    """O [B, Hq, M, d] and LSE [B, Hq, M] (fp64) of the newest rows over a
+    cache, one row at a time over the rows it sees; with ``Kp``, ``Vp``
+    [1, Hkv, P, d] every row also sees the whole shared prefix.  Rows that are
+    not computed stay NaN; a row that sees nothing gives 0 and -inf."""
+    B, Hq, M, d = Q.shape
+    G = Hq // K.shape[1]
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    O = np.full((B, Hq, M, d), np.nan, F64)
+    lse = np.full((B, Hq, M), np.nan, F64)
+    for b, r, pos in _cache_rows(B, M, K.shape[2], kv_len, q_len):
+        see = visible_keys(pos, window, n_sink)
+        for h in range(Hq):
+            k, v = K[b, h // G][see].astype(F64), V[b, h // G][see].astype(F64)
+            if Kp is not None:
+                k = np.concatenate([Kp[0, h // G].astype(F64), k])
+                v = np.concatenate([Vp[0, h // G].astype(F64), v])
+            if len(k) == 0:
+                O[b, h, r], lse[b, h, r] = 0.0, -np.inf
+                continue
+            x = scale * (k @ Q[b, h, r].astype(F64))
+            e = np.exp(x - x.max())
+            O[b, h, r] = (e @ v) / e.sum()
+            lse[b, h, r] = x.max() + np.log(e.sum())
+    return O, lse
+
+
+def key_mass(Q, K, lse, prev=None, decay: float = 1.0, window: int = 0, n_sink: int = 0, kv_len=None, q_len=None,
+             scale: Optional[float] = None) -> np.ndarray:
+    """mass [B, Hkv, N] (fp64): decayed earlier mass plus exp(logit - lse) of
+    every row that sees the key; 0 at and after kv_len."""
+    B, Hq, M, d = Q.shape
+    Hkv, N = K.shape[1], K.shape[2]
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    mass = np.zeros((B, Hkv, N), F64)
+    for b in range(B):
+        L = N if kv_len is None else int(kv_len[b])
+        if prev is not None:
+            mass[b, :, :L] = decay * prev[b, :, :L].astype(F64)
+    for b, r, pos in _cache_rows(B, M, N, kv_len, q_len):
+        see = visible_keys(pos, window, n_sink)
+        for h in range(Hq):
+            if lse[b, h, r] == -np.inf:
+                continue
+            hk = h // (Hq // Hkv)
+            x = scale * (K[b, hk][see].astype(F64) @ Q[b, h, r].astype(F64))
+            mass[b, hk][see] += np.exp(x - float(lse[b, h, r]))
+    return mass
+
+
+def evict(mass, budget: int, recent: int = 0, n_sink: int = 0, kv_len=None) -> np.ndarray:
+    """keep [B, Hkv, budget] int32: the kept positions, ascending, -1 after the
+    last: the first ``n_sink`` and last ``recent`` keys, then by descending
+    mass (NaN lowest), ties to the lower position."""
+    B, Hkv, N = mass.shape
+    keep = np.full((B, Hkv, budget), -1, np.int32)
+    for b in range(B):
+        L = N if kv_len is None else int(kv_len[b])
+        for h in range(Hkv):
+            def rank(j):
+                always = j < n_sink or j >= L - recent
+                x = float(mass[b, h, j])
+                return (0 if always else 2 if math.isnan(x) else 1, 0.0 if always or math.isnan(x) else -x, j)
+            kept = sorted(sorted(range(L), key=rank)[:budget])
+            keep[b, h, :len(kept)] = kept
+    return keep

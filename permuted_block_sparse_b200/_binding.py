@@ -8,6 +8,7 @@ or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -21,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libpbs.so")
 PBS_OP_PERMUTE, PBS_OP_SELECT, PBS_OP_ATTN, PBS_OP_PERMUTE_SEGMENTED, PBS_OP_SELECT_SEGMENTED = 0, 1, 2, 3, 4
 PBS_OP_SELECT_SAMPLE = 5
 PBS_OP_PERMUTE_QUERIES = 6
+PBS_OP_ATTN_WINDOW, PBS_OP_ATTN_PREFIX, PBS_OP_KEY_MASS, PBS_OP_EVICT = 7, 8, 9, 10
 PBS_SELECT_TOPK, PBS_SELECT_TAU, PBS_SELECT_SAMPLE = 0, 1, 2
 _MODES = {"topk": PBS_SELECT_TOPK, "tau": PBS_SELECT_TAU, "sample": PBS_SELECT_SAMPLE}
 PBS_SELECT_SCORE_ORDER, PBS_SELECT_PERM_PER_SEGMENT = 0x10, 0x20
@@ -30,7 +32,8 @@ STATUS = {0: "PBS_OK", -1: "PBS_ERR_INVALID_ARG", -2: "PBS_ERR_UNSUPPORTED", -3:
 EXPORTS = ("pbs_workspace_size", "pbs_permute", "pbs_permute_segmented", "pbs_select_capacity", "pbs_select",
            "pbs_attn_fwd", "pbs_attn_fwd_early_stop", "pbs_attn_fwd_ex", "pbs_check_device",
            "pbs_get_last_error", "pbs_version", "pbs_permute_noalloc", "pbs_test_inject_timeout",
-           "pbs_permute_queries", "pbs_select_qperm", "pbs_attn_fwd_qperm")
+           "pbs_permute_queries", "pbs_select_qperm", "pbs_attn_fwd_qperm",
+           "pbs_attn_window", "pbs_attn_prefix", "pbs_key_mass", "pbs_evict")
 
 
 class PbsError(RuntimeError):
@@ -84,6 +87,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pbs_select_qperm.restype = i32
     lib.pbs_attn_fwd_qperm.argtypes = [P, P, P, vp, vp, vp, vp, i32, i32, i32, ctypes.c_float, P, vp, vp, vp]
     lib.pbs_attn_fwd_qperm.restype = i32
+    f32 = ctypes.c_float
+    lib.pbs_attn_window.argtypes = [P, P, P, vp, vp, i64, i32, f32, P, vp, vp, sz, vp]
+    lib.pbs_attn_window.restype = i32
+    lib.pbs_attn_prefix.argtypes = [P, P, P, P, P, vp, vp, f32, P, vp, vp, sz, vp]
+    lib.pbs_attn_prefix.restype = i32
+    lib.pbs_key_mass.argtypes = [P, P, vp, vp, vp, i64, i32, f32, f32, vp, i64, vp, i64, vp, sz, vp]
+    lib.pbs_key_mass.restype = i32
+    lib.pbs_evict.argtypes = [vp, i64, P, P, vp, i32, i32, i32, vp, vp, P, P, vp, i64, vp, sz, vp]
+    lib.pbs_evict.restype = i32
     lib.pbs_test_inject_timeout.argtypes = [ctypes.c_uint]
     lib.pbs_test_inject_timeout.restype = None
     lib.pbs_get_last_error.argtypes = []
@@ -112,6 +124,9 @@ def describe(t: torch.Tensor) -> PbsTensor:
     B, H, N, D = t.shape
     sB, sH, sN, _ = t.stride()
     return PbsTensor(t.data_ptr(), B, H, N, D, sB, sH, sN)
+
+
+_HERE_AND_NOW = contextlib.nullcontext()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -362,6 +377,192 @@ def pbs_attn_fwd_early_stop(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, p
                                        float(stop_tau), float(softmax_scale), ctypes.byref(o), _ptr(lse),
                                        _ptr(stats), _stream(stream)))
     return out, lse
+
+
+# --------------------------------------------------------- cache operators
+def _place(stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
+    """Context in which a cache operator allocates and launches: the tensors'
+    device, and ``stream`` where one is given, so that what is allocated here
+    belongs to the stream that uses it."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return _HERE_AND_NOW
+
+
+def _lengths(name: str, t: Optional[torch.Tensor], B: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape ({B},)")
+    return t.data_ptr()
+
+
+def _int32(name: str, x: int) -> int:
+    if not -2 ** 31 <= x < 2 ** 31:          # ctypes would drop the upper bits
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def _row_stride(name: str, t: torch.Tensor, shape: Tuple[int, ...]) -> int:
+    """Elements between successive (b, hkv) rows of an fp32 [B, Hkv, n] tensor."""
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    sB, sH, sn = t.stride()
+    B, H, n = shape
+    if H == 1:
+        sH = sB if B > 1 else n
+    if (sn != 1 and n > 1) or (B > 1 and sB != H * sH):
+        raise ValueError(f"{name} must have unit stride within rows and evenly spaced (b, hkv) rows")
+    return sH
+
+
+def _check_out(name: str, t: torch.Tensor, dtype, shape: Tuple[int, ...]) -> None:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+
+
+def _cache_attn(Q, Kp, Vp, K, V, window, n_sink, kv_len, q_len, softmax_scale, out, lse, want_lse, ws, stream):
+    lib = load()
+    q, k, v = describe(Q), describe(K), describe(V)
+    B, Hq, M, D = Q.shape
+    kv, ql = _lengths("kv_len", kv_len, B), _lengths("q_len", q_len, B)
+    _int32("n_sink", n_sink)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    with _place(stream, Q, K, V, Kp, Vp, kv_len, q_len, out, lse, ws):
+        if out is None:
+            out = torch.empty((B, Hq, M, D), dtype=torch.bfloat16, device=Q.device)
+        if lse is not None:
+            _check_out("lse", lse, torch.float32, (B, Hq, M))
+        elif want_lse:
+            lse = torch.empty((B, Hq, M), dtype=torch.float32, device=Q.device)
+        if ws is None:
+            op = PBS_OP_ATTN_WINDOW if Kp is None else PBS_OP_ATTN_PREFIX
+            ws = _workspace(lib.pbs_workspace_size(op, q, k, 0, 0), Q.device)
+        wp, wn = _aligned(ws)
+        o, s = describe(out), _stream(stream)
+        if Kp is None:
+            rc = lib.pbs_attn_window(q, k, v, kv, ql, window, n_sink, softmax_scale, o, _ptr(lse), wp, wn, s)
+        else:
+            rc = lib.pbs_attn_prefix(q, describe(Kp), describe(Vp), k, v, kv, ql, softmax_scale, o, _ptr(lse), wp, wn,
+                                     s)
+    _check(rc)
+    return out, lse
+
+
+def pbs_attn_window(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int = 0, n_sink: int = 0,
+                    kv_len: Optional[torch.Tensor] = None, q_len: Optional[torch.Tensor] = None,
+                    softmax_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, want_lse: bool = True, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(O [B, Hq, M, D] bf16, LSE [B, Hq, M] fp32 or None) of the newest M
+    tokens over a cache of N keys per sequence, ``kv_len`` [B] int32 of them
+    filled: every row sees the last ``window`` keys up to its own (0: all) and
+    the first ``n_sink``.  With ``q_len`` [B] int32 only that many rows of each
+    sequence are queries; the other rows of the outputs are not written."""
+    return _cache_attn(Q, None, None, K, V, window, n_sink, kv_len, q_len, softmax_scale, out, lse, want_lse, ws,
+                       stream)
+
+
+def pbs_attn_prefix(Q: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                    kv_len: Optional[torch.Tensor] = None, q_len: Optional[torch.Tensor] = None,
+                    softmax_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, want_lse: bool = True, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(O, LSE) of a batch over one shared prefix ``Kp``, ``Vp``
+    [1, Hkv, P, D], read once for the batch, and each sequence's own cache
+    ``K``, ``V`` after it (lengths as for :func:`pbs_attn_window`)."""
+    if Kp is None or Vp is None:
+        raise ValueError("Kp and Vp are needed")
+    return _cache_attn(Q, Kp, Vp, K, V, 0, 0, kv_len, q_len, softmax_scale, out, lse, want_lse, ws, stream)
+
+
+def pbs_key_mass(Q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, mass: Optional[torch.Tensor] = None,
+                 decay: float = 1.0, window: int = 0, n_sink: int = 0, kv_len: Optional[torch.Tensor] = None,
+                 q_len: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+                 out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """[B, Hkv, N] fp32: ``decay`` times the earlier ``mass`` (None: zero) plus
+    the attention weight that the rows of ``Q`` give each key, from the ``lse``
+    of their attention.  ``out`` may be ``mass`` itself."""
+    lib = load()
+    q, k = describe(Q), describe(K)
+    B, Hq, M, D = Q.shape
+    shape = (B, K.shape[1], K.shape[2])
+    kv, ql = _lengths("kv_len", kv_len, B), _lengths("q_len", q_len, B)
+    _int32("n_sink", n_sink)
+    _check_out("lse", lse, torch.float32, (B, Hq, M))
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    s_in = 0 if mass is None else _row_stride("mass", mass, shape)
+    with _place(stream, Q, K, lse, mass, kv_len, q_len, out, ws):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=Q.device)
+        s_out = _row_stride("out", out, shape)
+        if ws is None:
+            ws = _workspace(lib.pbs_workspace_size(PBS_OP_KEY_MASS, q, k, 0, 0), Q.device)
+        wp, wn = _aligned(ws)
+        rc = lib.pbs_key_mass(q, k, lse.data_ptr(), kv, ql, window, n_sink, decay, softmax_scale, _ptr(mass), s_in,
+                              out.data_ptr(), s_out, wp, wn, _stream(stream))
+    _check(rc)
+    return out
+
+
+def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int, recent: int = 0, n_sink: int = 0,
+              kv_len: Optional[torch.Tensor] = None, keep: Optional[torch.Tensor] = None,
+              K_out: Optional[torch.Tensor] = None, V_out: Optional[torch.Tensor] = None,
+              mass_out: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, ...]:
+    """(keep [B, Hkv, budget] int32, K_out, V_out, mass_out, new_len [B] int32):
+    every cache cut to ``budget`` keys, of which the first ``n_sink`` and the
+    last ``recent`` always stay and the rest are those of highest ``mass``.
+    ``K_out`` and ``V_out`` [B, Hkv, n >= budget, D] and ``mass_out``
+    [B, Hkv, n >= budget] take the kept rows at their start."""
+    lib = load()
+    k, v = describe(K), describe(V)
+    B, Hkv, N, D = K.shape
+    kv = _lengths("kv_len", kv_len, B)
+    s_in = _row_stride("mass", mass, (B, Hkv, N))
+    if not 1 <= budget <= N:
+        raise ValueError(f"budget {budget} is not in [1, N = {N}]")
+    _int32("recent", recent), _int32("n_sink", n_sink)
+    with _place(stream, K, V, mass, kv_len, keep, K_out, V_out, mass_out, new_len, ws):
+        dev = K.device
+        if keep is None:
+            keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev)
+        else:
+            _check_out("keep", keep, torch.int32, (B, Hkv, budget))
+        if K_out is None:
+            K_out = torch.empty((B, Hkv, budget, D), dtype=torch.bfloat16, device=dev)
+        if V_out is None:
+            V_out = torch.empty((B, Hkv, K_out.shape[2], D), dtype=torch.bfloat16, device=dev)
+        if mass_out is None:
+            mass_out = torch.empty((B, Hkv, budget), dtype=torch.float32, device=dev)
+        s_out = _row_stride("mass_out", mass_out, (B, Hkv) + tuple(mass_out.shape[2:]))
+        if mass_out.shape[2] < budget:
+            raise ValueError(f"mass_out has room for {mass_out.shape[2]} of {budget} keys")
+        if new_len is None:
+            new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        else:
+            _check_out("new_len", new_len, torch.int32, (B,))
+        if ws is None:
+            ws = _workspace(lib.pbs_workspace_size(PBS_OP_EVICT, k, k, 0, 0), dev)
+        wp, wn = _aligned(ws)
+        rc = lib.pbs_evict(mass.data_ptr(), s_in, k, v, kv, budget, recent, n_sink, keep.data_ptr(),
+                           new_len.data_ptr(), describe(K_out), describe(V_out), mass_out.data_ptr(), s_out, wp, wn,
+                           _stream(stream))
+    _check(rc)
+    return keep, K_out, V_out, mass_out, new_len
 
 
 def pbs_check_device(stream=None) -> None:

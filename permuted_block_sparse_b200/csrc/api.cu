@@ -146,6 +146,10 @@ int api_ok() { return ok(); }
 
 int* api_device_error_word() { return device_error_word(); }
 
+int api_check_tensor(const pbs_tensor* t, const char* name, TensorDesc* out) { return check_tensor(t, name, out); }
+
+int api_check_ws(void* ws, size_t ws_bytes, size_t need) { return check_ws(ws, ws_bytes, need); }
+
 int api_validate_permute(const pbs_tensor* Qt, const pbs_tensor* Kt, int blk, int seg, int n_sink,
                          const int32_t* perm, TensorDesc* Q, TensorDesc* K) {
   int rc;
@@ -225,6 +229,17 @@ const char* pbs_get_last_error(void) { return g_last_error.c_str(); }
 size_t pbs_workspace_size(int op, const pbs_tensor* Qt, const pbs_tensor* Kt, int blk, int seg) {
   pbs::TensorDesc Q, K;
   if (check_tensor(Qt, "Q", &Q) || check_tensor(Kt, "K", &K)) return 0;
+  switch (op) {
+    case PBS_OP_ATTN_WINDOW:
+    case PBS_OP_ATTN_PREFIX:
+      return align256(pbs::cache_attn_ws_bytes(Q, K, op == PBS_OP_ATTN_PREFIX));
+    case PBS_OP_KEY_MASS:
+      return align256(pbs::key_mass_ws_bytes(Q, K));
+    case PBS_OP_EVICT:
+      return align256(pbs::evict_ws_bytes(K));
+    default:
+      break;
+  }
   if (blk != 64 && blk != 128) return 0;
   const int64_t nseg = seg > 0 ? (K.N + seg - 1) / seg : 0;
   switch (op) {

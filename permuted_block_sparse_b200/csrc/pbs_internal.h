@@ -61,6 +61,8 @@ cudaError_t launch_select_blocks(const SelectParams& p, const float* qbar, const
 int api_fail(int code, const char* msg);
 int api_ok();
 int* api_device_error_word();
+int api_check_tensor(const pbs_tensor* t, const char* name, TensorDesc* out);
+int api_check_ws(void* ws, size_t ws_bytes, size_t need);
 int api_validate_permute(const pbs_tensor* Qt, const pbs_tensor* Kt, int blk, int seg, int n_sink,
                          const int32_t* perm, TensorDesc* Q, TensorDesc* K);
 
@@ -91,5 +93,55 @@ cudaError_t launch_attn_fwd(const AttnParams& p, cudaStream_t s);
 // launch_attn_fwd where it applies.
 bool attn_fwd_pair_applies(const AttnParams& p);
 cudaError_t launch_attn_fwd_pair(const AttnParams& p, cudaStream_t s);
+
+// Cache operators ---------------------------------------------------------
+// Which keys a query row sees: rows r < q_len stand at pos = kv_len - q_len
+// + r and see keys j <= pos with j > pos - window or j < n_sink.
+struct CacheMask {
+  const int32_t* kv_len;  // NULL: N
+  const int32_t* q_len;   // NULL: M
+  int64_t window;         // at most N; N where there is no window
+  int n_sink;             // at most N
+};
+struct CacheAttnParams {
+  TensorDesc Q, K, V, O;
+  TensorDesc Kp, Vp;      // shared prefix (P = Kp.N keys); Kp.ptr NULL: none
+  CacheMask mask;
+  float scale_log2;       // softmax scale * log2(e)
+  float* lse;             // NULL if not wanted
+  void* ws;
+  int* err;
+};
+size_t cache_attn_ws_bytes(const TensorDesc& Q, const TensorDesc& K, bool prefix);
+cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s);
+
+struct KeyMassParams {
+  TensorDesc Q, K;
+  CacheMask mask;
+  const float* lse;
+  const float* prev;      // NULL: none
+  int64_t prev_stride, mass_stride;
+  float decay, scale_log2;
+  float* mass;
+  void* ws;
+  int* err;
+};
+size_t key_mass_ws_bytes(const TensorDesc& Q, const TensorDesc& K);
+cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t s);
+
+struct EvictParams {
+  TensorDesc K, V, Ko, Vo;
+  const float* mass;
+  int64_t mass_stride, mass_out_stride;
+  const int32_t* kv_len;
+  int budget, recent, n_sink;
+  int32_t* keep;
+  int32_t* new_len;       // NULL if not wanted
+  float* mass_out;
+  void* ws;
+  int* err;
+};
+size_t evict_ws_bytes(const TensorDesc& K);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 
 }  // namespace pbs
