@@ -15,8 +15,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpbs.so")
 SOURCES = ["api.cu", "permute.cu", "permute_seg.cu", "select.cu", "select_sample.cu", "attn_fwd.cu",
            "attn_fwd_pair.cu", "permute_queries.cu",
-           "permute_noalloc.cu", "cache_api.cu", "cache_attn.cu", "key_mass.cu", "evict.cu"]
-HEADERS = ["pbs_common.cuh", "pbs_internal.h", "cache_common.cuh"]
+           "permute_noalloc.cu", "cache_api.cu", "cache_attn.cu", "cache_attn_wide.cu", "key_mass.cu", "evict.cu"]
+HEADERS = ["pbs_common.cuh", "pbs_internal.h", "cache_common.cuh", "cache_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 

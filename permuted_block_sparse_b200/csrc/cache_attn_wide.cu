@@ -1,0 +1,601 @@
+// Attention over a K/V cache for many query rows (prompts, chunks, and a
+// batch's rows over a shared prefix): the tcgen05 kernel of pbs_attn_window
+// and pbs_attn_prefix.
+//
+// Tile layout.  128 MMA rows are query rows of ONE KV head packed as (sequence,
+// position, head of the group), head innermost: one TMA box {64 columns, G
+// heads, positions, sequences} lands them in that order.  So a tile spans only
+// 128 / G positions, and with a window of W keys it reads W + 128 / G keys where
+// a tile of 128 positions of one head would read W + 128; every K/V tile serves
+// the whole head group.  A CTA runs two such tiles (slots) over the union of
+// their keys, so each K/V tile is loaded once for 256 rows and one slot's
+// softmax runs while the tensor core works for the other.
+//
+// The keys a CTA needs are a run of virtual indices (KeyRun): sinks, then the
+// window, without the gap between them; the tile in which they meet is loaded
+// as 16-row boxes.  Tiles start at the first needed key, not at a multiple of
+// 128.
+//
+// Roles (384 threads): warp 0 issues tcgen05.mma and owns tensor memory; warp
+// 1 issues the TMA loads of Q and of the K and V rings; warps 2-3 clean the V
+// tiles that some row must not see in full (below); warps 4-7 and 8-11 run the
+// softmax of slot 0 and 1, one row per thread.  Tensor memory (512 columns):
+// S0 | S1 | O0 | O1; P (bf16) overwrites S and is the A operand of PV.  The
+// order of MMAs is fixed: PV of a slot's tile, then QK^T of its next tile, slots
+// in turn.
+//
+// A masked key has weight 0, but 0 * NaN is NaN: where a tile holds a key that
+// some row of the CTA does not see, warps 2-3 replace NaN and infinities in V
+// by 0 before the product and note the key; at the end each row that does see
+// such a key takes those entries from global memory.
+//
+// Bound: the softmax.  A 128 x 128 tile costs 2 x 256 clocks of tensor core and
+// 1024 of the SM's 16 exponentials per clock; with few rows per CTA, HBM.
+#include <math.h>
+
+#include <algorithm>
+
+#include "cache_attn.cuh"
+
+namespace pbs {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr float kRescaleSlack = 8.0f;   // keep the running max while within 2^8
+// Tiles of a CTA that some row does not see in full: two per slot at the causal
+// end and two at the window's start (a slot spans at most 128 positions), one
+// at the end of the sinks.
+constexpr int kMaxDirty = 9;
+
+template <int D>
+struct WideCfg {
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kTile = (D / 64) * 128 * 128;   // Q, K or V tile: 64-column halves of 128-byte rows
+  static constexpr int kQ = 0;
+  static constexpr int kK = 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kBytes = kV + kStages * kTile + 1024;   // alignment slack
+};
+
+// How query rows are packed into tiles.
+struct WideRows {
+  int pos_per_tile, seqs_per_tile, tiles;   // tiles per sequence, or in all over a prefix
+};
+
+__host__ __device__ __forceinline__ WideRows wide_rows(int64_t B, int64_t M, int64_t G, bool prefix) {
+  WideRows w;
+  const int64_t most = 128 / G;
+  w.pos_per_tile = static_cast<int>(M < most ? M : most);
+  w.seqs_per_tile = 1;
+  if (prefix && M <= most) {
+    const int64_t n = 128 / (G * M);
+    w.seqs_per_tile = static_cast<int>(n < B ? n : B);
+    w.tiles = static_cast<int>((B + w.seqs_per_tile - 1) / w.seqs_per_tile);
+  } else {
+    w.tiles = static_cast<int>((M + w.pos_per_tile - 1) / w.pos_per_tile * (prefix ? B : 1));
+  }
+  return w;
+}
+
+// Rescale the first n16 x 16 P columns of this tile (bf16 pairs) by beta, after
+// this thread's earlier P stores have landed (rare; whole warps).
+__device__ __noinline__ void rescale_p(uint32_t tS, int n16, float beta) {
+  tmem_st_wait();
+  for (int q = 0; q < n16; ++q) {
+    uint32_t w[16];
+    tmem_ld16(tS + q * 16, w);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+      w[e] = pack_bf16x2(f.x * beta, f.y * beta);
+    }
+    tmem_st16(tS + q * 16, w);
+  }
+}
+template <int D>
+__device__ __noinline__ void rescale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t u[32];
+    tmem_ld32(tO + c * 32, u);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+    tmem_st32(tO + c * 32, u);
+  }
+}
+
+template <int NS>
+struct Shared {
+  uint64_t bar_q, bar_k[NS], bar_v[NS], bar_vraw[NS], bar_kempty[NS], bar_vempty[NS];
+  uint64_t bar_s[2], bar_p[2], bar_o[2], bar_fin;
+  uint32_t tmem_base;
+  int abort;
+  int n_dirty;                            // tiles cleaned, and whether any held something
+  int any_bad;
+  int dirty_tile[kMaxDirty];
+  uint32_t bad[kMaxDirty][4];             // their keys with NaN or infinities in V
+};
+
+struct WideMaps {
+  CUtensorMap q, k, v, k16, v16;          // boxes of 128 key rows, and of 16
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnParams p, const AttnParts parts,
+                                                                const bool prefix, const WideRows wr,
+                                                                const __grid_constant__ WideMaps maps) {
+  using C = WideCfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  __shared__ Shared<NS> sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int M = static_cast<int>(p.Q.N), Hq = static_cast<int>(p.Q.H), Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
+  const int B = static_cast<int>(p.Q.B);
+
+  // ---- this CTA's work: a pair of tiles, a KV head (and sequence), a part of the keys
+  const int n_parts = prefix ? parts.prefix : parts.own;
+  const int pairs = (wr.tiles + 1) / 2;
+  const int part = static_cast<int>(blockIdx.x) % n_parts;
+  const int rest = static_cast<int>(blockIdx.x) / n_parts;
+  const int pair = pairs - 1 - rest % pairs;          // without a window later positions have more keys: first
+  const int hk = rest / pairs % Hkv;
+  const int b_own = prefix ? 0 : rest / pairs / Hkv;
+  const int nq_own = prefix ? M : cache_len(p.mask.q_len, b_own, M, p.err);
+  const int L = prefix ? static_cast<int>(p.Kp.N) : cache_len(p.mask.kv_len, b_own, p.K.N, p.err);
+  const int n_pos_tiles = (M + wr.pos_per_tile - 1) / wr.pos_per_tile;   // per sequence
+  // first sequence and first row of each slot's tile
+  auto tile_seq = [&](int h) {
+    const int t = 2 * pair + h;
+    return prefix ? (wr.seqs_per_tile > 1 || n_pos_tiles == 1 ? t * wr.seqs_per_tile : t / n_pos_tiles) : b_own;
+  };
+  auto tile_row = [&](int h) {
+    const int t = 2 * pair + h;
+    return (prefix ? (n_pos_tiles == 1 ? 0 : t % n_pos_tiles) : t) * wr.pos_per_tile;
+  };
+  auto has_rows = [&](int h) { return 2 * pair + h < wr.tiles && tile_row(h) < nq_own; };
+  if (!has_rows(0)) return;                           // (slot 1 then has none either)
+  const int n_slot = has_rows(1) ? 2 : 1;
+  // positions of the slots' first and last rows (own keys)
+  auto first_pos = [&](int h) { return L - nq_own + tile_row(h); };
+  auto last_pos = [&](int h) { return L - nq_own + min(tile_row(h) + wr.pos_per_tile, nq_own) - 1; };
+  const KeyRun run = prefix ? KeyRun{0, 0, 0, L}
+                            : key_run<16>(first_pos(0), last_pos(n_slot - 1), p.mask.window, p.mask.n_sink);
+  const int T = (run.n + 127) / 128;
+  const int t0 = static_cast<int>(static_cast<int64_t>(T) * part / n_parts);
+  const int t1 = static_cast<int>(static_cast<int64_t>(T) * (part + 1) / n_parts);
+  // does slot h see any key of tile t, and do all its rows see all of them?
+  int hi_first[2], hi_last[2], lo_first[2], lo_last[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    hi_first[h] = hi_last[h] = prefix ? L - 1 : 0;
+    lo_first[h] = lo_last[h] = 0;
+    if (!prefix && h < n_slot) {
+      hi_first[h] = run.hi(first_pos(h));
+      hi_last[h] = run.hi(last_pos(h));
+      lo_first[h] = run.lo(first_pos(h), p.mask.window);
+      lo_last[h] = run.lo(last_pos(h), p.mask.window);
+    }
+  }
+  auto active = [&](int h, int t) {
+    return h < n_slot && 128 * t <= hi_last[h] && (128 * t + 127 >= lo_first[h] || 128 * t < run.n_sink);
+  };
+  auto full = [&](int h, int t) {
+    return 128 * t + 127 <= hi_first[h] && (128 * t >= lo_last[h] || 128 * t + 127 < run.n_sink);
+  };
+  // (rows past the prefix are zeros, never NaN: no cleaning there)
+  auto dirty = [&](int t) {
+    return !prefix && ((active(0, t) && !full(0, t)) || (active(1, t) && !full(1, t)));
+  };
+
+  const uint32_t sQ = smem_u32(smem + C::kQ), sK = smem_u32(smem + C::kK), sV = smem_u32(smem + C::kV);
+  if (tid == 32) {
+    sh.abort = 0;
+    sh.n_dirty = 0;
+    sh.any_bad = 0;
+    for (int i = 0; i < kMaxDirty * 4; ++i) sh.bad[i / 4][i % 4] = 0u;
+    mbar_init(&sh.bar_q, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sh.bar_k[i], 1);
+      mbar_init(&sh.bar_v[i], 1);
+      mbar_init(&sh.bar_vraw[i], 1);
+      mbar_init(&sh.bar_kempty[i], 1);
+      mbar_init(&sh.bar_vempty[i], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sh.bar_s[h], 1);
+      mbar_init(&sh.bar_p[h], 4);
+      mbar_init(&sh.bar_o[h], 1);
+    }
+    mbar_init(&sh.bar_fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* abort_flag = &sh.abort;
+
+  if (warp == 1) {
+    // ============================================================ producer
+    if (lane == 0) {
+      const int box = wr.pos_per_tile * wr.seqs_per_tile * G * 128;     // bytes of a 64-column Q box
+      mbar_expect_tx(&sh.bar_q, static_cast<uint32_t>(n_slot * (D / 64) * box));
+      for (int h = 0; h < n_slot; ++h)
+        for (int c = 0; c < D / 64; ++c)
+          tma_rows_4d(sQ + h * C::kTile + c * (128 * 128), &maps.q, c * 64, hk * G, tile_row(h), tile_seq(h), &sh.bar_q);
+      // a K or V tile: one box per 64 columns, or 16-row boxes where it spans
+      // the end of the sinks (broadcast heads or sequences are one in the map)
+      const int kh = (prefix ? p.Kp.sH : p.K.sH) == 0 ? 0 : hk, vh = (prefix ? p.Vp.sH : p.V.sH) == 0 ? 0 : hk;
+      const int kbt = p.K.sB == 0 ? 0 : b_own, vbt = p.V.sB == 0 ? 0 : b_own;
+      auto tile = [&](uint32_t dst, const CUtensorMap* one, const CUtensorMap* rows16, int head, int seq, int t,
+                      uint64_t* bar) {
+        mbar_expect_tx(bar, static_cast<uint32_t>(C::kTile));
+        const int v0 = 128 * t;
+        const bool mixed = run.delta > 0 && v0 < run.sink_end && v0 + 128 > run.sink_end;
+        for (int c = 0; c < D / 64; ++c) {
+          const uint32_t d = dst + c * (128 * 128);
+          if (!mixed) {
+            tma_rows_4d(d, one, c * 64, run.key(v0), head, seq, bar);
+          } else {
+            for (int r = 0; r < 128; r += 16) tma_rows_4d(d + r * 128, rows16, c * 64, run.key(v0 + r), head, seq, bar);
+          }
+        }
+      };
+      int nk = t0, nv = t0, raw[NS] = {};             // tiles issued; of them through bar_vraw, per stage
+      for (int t = t0; t < t1; ++t) {
+        const int i = t - t0, st = i % NS;
+        const uint32_t again = ((i / NS) - 1) & 1;
+        if (i >= NS && !mbar_wait_or_abort(&sh.bar_kempty[st], again, p.err, abort_flag)) break;
+        tile(sK + st * C::kTile, &maps.k, &maps.k16, kh, kbt, t, &sh.bar_k[st]);
+        ++nk;
+        if (i >= NS && !mbar_wait_or_abort(&sh.bar_vempty[st], again, p.err, abort_flag)) break;
+        const bool d = dirty(t);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) raw[q] += d && q == st;
+        tile(sV + st * C::kTile, &maps.v, &maps.v16, vh, vbt, t, d ? &sh.bar_vraw[st] : &sh.bar_v[st]);
+        ++nv;
+      }
+      // no copy may be in flight when the CTA ends; without an abort the MMA
+      // role has waited for all of them
+      if (*abort_flag) {
+        mbar_wait(&sh.bar_q, 0, p.err);
+        for (int t = max(t0, nk - NS); t < nk; ++t) mbar_wait(&sh.bar_k[(t - t0) % NS], ((t - t0) / NS) & 1, p.err);
+        for (int t = max(t0, nv - NS); t < nv; ++t) {
+          const int st = (t - t0) % NS;
+          int fills = 0;
+#pragma unroll
+          for (int q = 0; q < NS; ++q)
+            if (q == st) fills = raw[q];
+          if (dirty(t)) mbar_wait(&sh.bar_vraw[st], (fills - 1) & 1, p.err);
+          else mbar_wait(&sh.bar_v[st], ((t - t0) / NS) & 1, p.err);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ========================================================= MMA issuer
+    // (all lanes wait, so that each has acquired what it issues on)
+    constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false), idesc_pv = idesc_bf16(128, D, true);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, p.err, abort_flag));
+      tc_fence_after();
+    };
+    wait(&sh.bar_q, 0);
+    int k_seen = t0, v_seen = t0;           // tiles below have landed (waited for in order)
+    auto landed = [&](uint64_t* bars, int& seen, int t) {
+      for (; ok && seen <= t; ++seen) wait(&bars[(seen - t0) % NS], ((seen - t0) / NS) & 1);
+    };
+    auto last_user = [&](int h, int t) { return h == 1 || !active(1, t); };
+    int done[2] = {0, 0};                   // tiles whose QK^T has been issued, per slot
+    auto qk = [&](int h, int t) {
+      landed(sh.bar_k, k_seen, t);
+      if (!ok) return;
+      const int st = (t - t0) % NS;
+      const uint64_t a0 = sdesc_sw128(sQ + h * C::kTile, 16, 1024);
+      const uint64_t b0 = sdesc_sw128(sK + st * C::kTile, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * (128 * 128) + (kk % 4) * 32;
+        if (elect_one()) mma_ss(tmem + h * 128, sdesc_add(a0, off), sdesc_add(b0, off), idesc_qk, kk > 0 ? 1u : 0u);
+      }
+      if (elect_one()) {
+        tc_commit(&sh.bar_s[h]);
+        if (last_user(h, t)) tc_commit(&sh.bar_kempty[st]);
+      }
+      __syncwarp();
+      ++done[h];
+    };
+    auto next = [&](int h, int t) {
+      while (t < t1 && !active(h, t)) ++t;
+      return t;
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = next(h, t0);
+      if (h < n_slot && t < t1) qk(h, t);
+    }
+    bool o_init[2] = {false, false};
+    for (int t = t0; ok && t < t1; ++t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!ok || !active(h, t)) continue;
+        wait(&sh.bar_p[h], (done[h] - 1) & 1);
+        landed(sh.bar_v, v_seen, t);
+        if (!ok) break;
+        const int st = (t - t0) % NS;
+        const uint64_t b0 = sdesc_sw128(sV + st * C::kTile, 128 * 128, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (elect_one())
+            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, sdesc_add(b0, kk * 2048), idesc_pv,
+                   kk > 0 || o_init[h] ? 1u : 0u);
+        o_init[h] = true;
+        if (last_user(h, t) && elect_one()) tc_commit(&sh.bar_vempty[st]);
+        __syncwarp();
+        const int tn = next(h, t + 1);
+        if (tn < t1) qk(h, tn);
+      }
+    }
+    if (elect_one()) {
+      tc_commit(&sh.bar_o[0]);
+      tc_commit(&sh.bar_o[1]);
+      tc_commit(&sh.bar_fin);
+    }
+    __syncwarp();
+    mbar_wait(&sh.bar_fin, 0, p.err);       // every MMA has completed before tensor memory is freed
+  } else if (warp < 4) {
+    // ===================================================== cleaning of V tiles
+    const int x = tid - 64;
+    int seen[NS] = {}, n_dirty = 0;
+    for (int t = t0; t < t1 && n_dirty < kMaxDirty; ++t) {
+      if (!dirty(t)) continue;
+      const int st = (t - t0) % NS;
+      int fill = 0;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i == st) fill = seen[i]++;
+      const bool got = mbar_wait_or_abort(&sh.bar_vraw[st], fill & 1, p.err, abort_flag);
+      if (named_sync_or(4, 64, !got)) break;
+      // thread x reads the same 16-byte chunks of rows x / 8, x / 8 + 8, ... of each half
+      uint4* v = reinterpret_cast<uint4*>(smem + C::kV + st * C::kTile);
+#pragma unroll 4
+      for (int i = x; i < C::kTile / 16; i += 64) {
+        uint4 w = v[i];
+        if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) | nonfinite_bf16x2(w.w)) {
+          w.x = finite_or_zero_bf16x2(w.x);
+          w.y = finite_or_zero_bf16x2(w.y);
+          w.z = finite_or_zero_bf16x2(w.z);
+          w.w = finite_or_zero_bf16x2(w.w);
+          v[i] = w;
+          const int row = i / 8 % 128;
+          if (128 * t + row < run.n) {
+            atomicOr(&sh.bad[n_dirty][row >> 5], 1u << (row & 31));
+            sh.any_bad = 1;
+          }
+        }
+      }
+      if (x == 0) {
+        sh.dirty_tile[n_dirty] = t;
+        sh.n_dirty = n_dirty + 1;
+      }
+      ++n_dirty;
+      fence_proxy_async();
+      named_sync(4, 64);
+      if (x == 0) mbar_arrive(&sh.bar_v[st]);
+    }
+  } else {
+    // ============================================================ softmax
+    const int h = (warp - 4) >> 2;
+    const int i = tid - 128 - h * 128;                // row of the tile = tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + h * 128 + lane_off, tO = tmem + 256 + h * 128 + lane_off;
+    // the query row of this thread
+    const int bb = tile_seq(h) + i / (wr.pos_per_tile * G), r = tile_row(h) + i / G % wr.pos_per_tile;
+    bool valid = h < n_slot && i < wr.pos_per_tile * wr.seqs_per_tile * G && bb < B && r < M;
+    if (valid) valid = r < (prefix ? cache_len(p.mask.q_len, bb, M, p.err) : nq_own);
+    const int pos = L - nq_own + r;
+    const int hi = prefix ? L - 1 : run.hi(pos), lo = prefix ? 0 : run.lo(pos, p.mask.window);
+    float m_run = -INFINITY, l_run = 0.f;
+    bool o_init = false, ok = true;
+    int k = 0;
+    for (int t = t0; t < t1; ++t) {
+      if (!active(h, t)) continue;
+      if (!mbar_wait_or_abort(&sh.bar_s[h], k & 1, p.err, abort_flag)) ok = false;
+      tc_fence_after();
+      const bool masked = !full(h, t);
+      float psum = 0.f, m_t = m_run;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t x[64], u[32];
+        tmem_ld64(tS + c * 64, x);
+        if (masked) {
+          // indices v0 + e <= hi with v0 + e < n_sink or >= lo
+          const int v0 = 128 * t + c * 64, e_hi = hi - v0, e_lo = lo - v0, e_s = run.n_sink - v0;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e > e_hi || (e < e_lo && e >= e_s)) x[e] = __float_as_uint(-INFINITY);
+        }
+        float mm[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          mm[q] = fmax3(__uint_as_float(x[q]), __uint_as_float(x[8 + q]), __uint_as_float(x[16 + q]));
+          mm[q] = fmax3(mm[q], __uint_as_float(x[24 + q]), __uint_as_float(x[32 + q]));
+          mm[q] = fmax3(mm[q], __uint_as_float(x[40 + q]), __uint_as_float(x[48 + q]));
+          mm[q] = fmaxf(mm[q], __uint_as_float(x[56 + q]));
+        }
+        const float cm =
+            fmax3(fmax3(mm[0], mm[1], mm[2]), fmax3(mm[3], mm[4], mm[5]), fmaxf(mm[6], mm[7])) * p.scale_log2;
+        const bool up = cm > (m_t == -INFINITY ? -INFINITY : m_t + kRescaleSlack);
+        if (__any_sync(0xffffffffu, up)) {
+          const float m_new = up ? cm : m_t;
+          const float beta = m_new == -INFINITY ? 1.0f : ex2(m_t - m_new);
+          if (c > 0 && __any_sync(0xffffffffu, beta != 1.0f)) rescale_p(tS, 2 * c, beta);
+          psum *= beta;
+          m_t = m_new;
+        }
+        const float m_use = m_t == -INFINITY ? 0.f : m_t;
+        unsigned long long ps2[4] = {0ull, 0ull, 0ull, 0ull};
+        const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const unsigned long long y =
+              f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2);
+          float y0, y1;
+          f2_unpack(y, y0, y1);
+          const float a0 = ex2(y0), a1 = ex2(y1);
+          ps2[e & 3] = f2_add(ps2[e & 3], f2_pack(a0, a1));
+          u[e] = cvt_bf16x2(a0, a1);
+        }
+        float s0, s1, s2, s3, s4, s5, s6, s7;
+        f2_unpack(ps2[0], s0, s1);
+        f2_unpack(ps2[1], s2, s3);
+        f2_unpack(ps2[2], s4, s5);
+        f2_unpack(ps2[3], s6, s7);
+        psum += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
+        tmem_st32(tS + c * 32, u);
+      }
+      const float alpha = m_t == -INFINITY ? 1.0f : ex2(m_run - m_t);
+      // (PV of this slot's previous tile has completed: the S-ready barrier
+      // tracks every MMA issued before this tile's QK^T)
+      if (o_init && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o<D>(tO, alpha);
+      l_run = l_run * alpha + psum;
+      m_run = m_t;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.bar_p[h]);
+      o_init = true;
+      ++k;
+    }
+    // ---- epilogue
+    if (h < n_slot) {
+      if (k > 0 && !mbar_wait_or_abort(&sh.bar_o[h], 0, p.err, abort_flag)) ok = false;
+      tc_fence_after();
+      ok = !named_sync_or(2 + h, 128, !ok);
+      const int n_all = parts.prefix + parts.own, slot = prefix ? part : parts.prefix + part;
+      const int64_t out = (static_cast<int64_t>(bb) * Hq + hk * G + i % G) * M + r;
+      const int n_dirty = sh.any_bad ? sh.n_dirty : 0;
+      if (!valid || k == 0) l_run = 0.f;
+      const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(const_cast<void*>(p.O.ptr)) + bb * p.O.sB +
+                         (hk * G + i % G) * p.O.sH + r * p.O.sN;
+      float* acc = parts.acc + (out * n_all + slot) * D;
+#pragma unroll 1
+      for (int c = 0; ok && c < D / 32; ++c) {
+        uint32_t u[32];
+        if (k > 0) {
+          tmem_ld32(tO + c * 32, u);
+        }
+        if (!valid) continue;
+        if (l_run == 0.f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[e] = 0u;
+        }
+        for (int q = 0; q < n_dirty * 128; ++q) {
+          if (!((sh.bad[q / 128][q / 32 % 4] >> (q % 32)) & 1u)) continue;
+          const int v = 128 * sh.dirty_tile[q / 128] + q % 128;
+          if (v > hi || (v < lo && v >= run.n_sink)) continue;
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.V.ptr) + b_own * p.V.sB + hk * p.V.sH +
+                                    static_cast<int64_t>(run.key(v)) * p.V.sN + c * 32;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float f = __bfloat162float(vr[e]);
+            if (!isfinite(f)) u[e] = __float_as_uint(__uint_as_float(u[e]) + f);
+          }
+        }
+        if (n_all == 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(u[e + 0]) * inv, __uint_as_float(u[e + 1]) * inv);
+            w.y = pack_bf16x2(__uint_as_float(u[e + 2]) * inv, __uint_as_float(u[e + 3]) * inv);
+            w.z = pack_bf16x2(__uint_as_float(u[e + 4]) * inv, __uint_as_float(u[e + 5]) * inv);
+            w.w = pack_bf16x2(__uint_as_float(u[e + 6]) * inv, __uint_as_float(u[e + 7]) * inv);
+            *reinterpret_cast<uint4*>(o + c * 32 + e) = w;
+          }
+        } else if (l_run != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(acc + c * 32 + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+        }
+      }
+      if (valid && ok) {
+        if (n_all > 1)
+          parts.ml[out * n_all + slot] = make_float2(l_run == 0.f ? -INFINITY : m_run, l_run);
+        else if (p.lse)
+          p.lse[out] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Tensor map over dims (D, d1, d2, d3) of a bf16 tensor with the given element
+// strides; extents of broadcast (zero-stride) dimensions are 1.  Strides of
+// extent-1 dimensions are never used and replaced by valid ones.
+bool encode(CUtensorMap* map, const void* ptr, int64_t D, const int64_t (&ext)[3], const int64_t (&str)[3],
+            const int (&box)[3]) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), 1, 1, 1}, strides[3];
+  cuuint32_t boxes[4] = {64, 1, 1, 1}, ones[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = str[i] == 0 ? 1 : static_cast<cuuint64_t>(ext[i]);
+    strides[i] = 2 * static_cast<cuuint64_t>(dims[i + 1] == 1 ? D : str[i]);
+    boxes[i + 1] = static_cast<cuuint32_t>(box[i]);
+  }
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_keys(CUtensorMap* map, const TensorDesc& t, int rows) {
+  return encode(map, t.ptr, t.D, {t.N, t.H, t.B}, {t.sN, t.sH, t.sB}, {rows, 1, 1});
+}
+
+template <int D>
+cudaError_t launch(const CacheAttnParams& p, const AttnParts& parts, bool prefix, cudaStream_t s) {
+  const TensorDesc& K = prefix ? p.Kp : p.K;
+  const TensorDesc& V = prefix ? p.Vp : p.V;
+  const int G = static_cast<int>(p.Q.H / p.K.H);
+  const WideRows wr = wide_rows(p.Q.B, p.Q.N, G, prefix);
+  WideMaps maps;
+  if (!encode(&maps.q, p.Q.ptr, D, {p.Q.H, p.Q.N, p.Q.B}, {p.Q.sH, p.Q.sN, p.Q.sB},
+              {G, wr.pos_per_tile, wr.seqs_per_tile}) ||
+      !encode_keys(&maps.k, K, 128) || !encode_keys(&maps.v, V, 128) || !encode_keys(&maps.k16, K, 16) ||
+      !encode_keys(&maps.v16, V, 16))
+    return cudaErrorNotSupported;
+  cudaError_t e = cudaFuncSetAttribute(attn_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       WideCfg<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = wide_units(p.Q, p.K, prefix) * (prefix ? parts.prefix : parts.own);
+  attn_wide_kernel<D><<<static_cast<unsigned>(ctas), kThreads, WideCfg<D>::kBytes, s>>>(p, parts, prefix, wr, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t wide_units(const TensorDesc& Q, const TensorDesc& K, bool prefix) {
+  const WideRows w = wide_rows(Q.B, Q.N, Q.H / K.H, prefix);
+  return (w.tiles + 1) / 2 * K.H * (prefix ? 1 : K.B);
+}
+
+cudaError_t launch_attn_wide(const CacheAttnParams& p, const AttnParts& parts, bool prefix, cudaStream_t s) {
+  return p.Q.D == 128 ? launch<128>(p, parts, prefix, s) : launch<64>(p, parts, prefix, s);
+}
+
+}  // namespace pbs

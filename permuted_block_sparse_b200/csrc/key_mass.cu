@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(kThreads) key_mass_row_kernel(KeyMassParams p)
     if (j >= L) continue;
     for (int i = 0; i < 8 && i0 + i < n_rows * G; ++i) {
       const int64_t r = (i0 + i) / G, h = hk * G + (i0 + i) % G;
-      if (!key_visible(j, L - n_rows + r, p.mask.window, p.mask.n_sink)) continue;
+      const int64_t pos = L - n_rows + r;
+      if (j > pos || (j <= pos - p.mask.window && j >= p.mask.n_sink)) continue;
       const float y = p.lse[(b * p.Q.H + h) * M + r];
       if (y == -INFINITY) continue;
       float s = 0.f;
