@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "cache_attn.cuh"
+#include "mma_sync.cuh"
 
 namespace pbs {
 namespace {
@@ -43,35 +44,6 @@ struct FewCfg {
   static constexpr int kBytes = kWarps * kRing;
 };
 
-// Byte offset of 16-byte chunk c of key row r: chunks XORed with the row, so
-// that the eight rows of an ldmatrix tile lie in different banks.
-template <int D>
-__device__ __forceinline__ uint32_t few_offset(int r, int c) {
-  return static_cast<uint32_t>(r * (D * 2) + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Two floats as bf16 pairs hi + lo: lo holds what the rounding of hi left.
-__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x, y);
-  const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi));
-  lo = pack_bf16x2(x - h.x, y - h.y);
-}
-
 // What each row of the CTA is, in shared memory.
 struct FewRow {
   int lo, hi;          // bounds of its visible indices (see KeyRun); hi < 0: none
@@ -92,7 +64,7 @@ __device__ __noinline__ void few_nonfinite(unsigned char* v, const FewRow* row, 
       for (int k = 0; k < kGroup; ++k) {
         const int i = v0 + k;
         if (i > me.hi || (i < me.lo && i >= n_sink)) continue;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(v + few_offset<D>(k, j) + (lane & 3) * 4);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(v + rows_offset<D>(k, j) + (lane & 3) * 4);
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
         if (!isfinite(f.x)) o[g][j][0] += f.x;
         if (!isfinite(f.y)) o[g][j][1] += f.y;
@@ -187,11 +159,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
         const int r = it * RPI + lr, v = v0 + r;
         const bool ok = v < end;
         const int64_t key = ok ? run.key(v) : 0;
-        cp_async16_zfill(dk + few_offset<D>(r, lc), kb + key * ksN + lc * 8, ok);
-        cp_async16_zfill(dv + few_offset<D>(r, lc), vb + key * vsN + lc * 8, ok);
+        cp_async16_zfill(dk + rows_offset<D>(r, lc), kb + key * ksN + lc * 8, ok);
+        cp_async16_zfill(dv + rows_offset<D>(r, lc), vb + key * vsN + lc * 8, ok);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
   };
 
   float o[NG][D / 8][4];
@@ -210,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
   for (int i = 0; i < kStages - 1; ++i) load(i, i);
   int st = 0;
   for (int i = 0; i < rounds; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    cp_async_wait<kStages - 2>();
     __syncwarp();                                 // the other lanes' copies too; and stage st - 1 is read
     load(i + kStages - 1, st == 0 ? kStages - 1 : st - 1);
     const int v0 = begin + (i * kWarps + warp) * kGroup;
@@ -222,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
     for (int k = 0; k < D / 16; ++k) {
       // matrices: keys 0-7 | 0-7 | 8-15 | 8-15, chunks 2k | 2k+1 | 2k | 2k+1
       uint32_t f[4];
-      ldsm4(f, sk + few_offset<D>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+      ldsm4(f, sk + rows_offset<D>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         mma_16816(s[t], qa[k][0], NG > 1 ? qa[k][NG - 1] : 0u, qa[k][NG], NG > 1 ? qa[k][2 * NG - 1] : 0u, f[2 * t],
@@ -278,7 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
     for (int j = 0; j < D / 16; ++j) {
       // matrices: keys 0-7 | 8-15 | 0-7 | 8-15, chunks 2j | 2j | 2j+1 | 2j+1
       uint32_t f[4];
-      ldsm4_t(f, sv + few_offset<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * j + (lane >> 4)));
+      ldsm4_t(f, sv + rows_offset<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * j + (lane >> 4)));
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         mma_16816(o[g][2 * j], ph[g][0], pl[g][0], ph[g][1], pl[g][1], f[0], f[1]);

@@ -39,7 +39,7 @@
 
 namespace pbs {
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // (select_sample.cu)
 
 namespace {
 
@@ -545,10 +545,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   }
 }
 
+template <int D>
+cudaError_t launch(const CacheAttnParams& p, const AttnParts& parts, bool prefix, cudaStream_t s) {
+  const TensorDesc& K = prefix ? p.Kp : p.K;
+  const TensorDesc& V = prefix ? p.Vp : p.V;
+  const int G = static_cast<int>(p.Q.H / p.K.H);
+  const WideRows wr = wide_rows(p.Q.B, p.Q.N, G, prefix);
+  WideMaps maps;
+  if (!encode_queries_map(&maps.q, p.Q, G, wr.pos_per_tile, wr.seqs_per_tile) ||
+      !encode_keys_map(&maps.k, K, 128) || !encode_keys_map(&maps.v, V, 128) || !encode_keys_map(&maps.k16, K, 16) ||
+      !encode_keys_map(&maps.v16, V, 16))
+    return cudaErrorNotSupported;
+  cudaError_t e = cudaFuncSetAttribute(attn_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       WideCfg<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = wide_units(p.Q, p.K, prefix) * (prefix ? parts.prefix : parts.own);
+  attn_wide_kernel<D><<<static_cast<unsigned>(ctas), kThreads, WideCfg<D>::kBytes, s>>>(p, parts, prefix, wr, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 // Tensor map over dims (D, d1, d2, d3) of a bf16 tensor with the given element
 // strides; extents of broadcast (zero-stride) dimensions are 1.  Strides of
 // extent-1 dimensions are never used and replaced by valid ones.
-bool encode(CUtensorMap* map, const void* ptr, int64_t D, const int64_t (&ext)[3], const int64_t (&str)[3],
+static bool encode_map(CUtensorMap* map, const void* ptr, int64_t D, const int64_t (&ext)[3], const int64_t (&str)[3],
             const int (&box)[3]) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
@@ -563,31 +584,13 @@ bool encode(CUtensorMap* map, const void* ptr, int64_t D, const int64_t (&ext)[3
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool encode_keys(CUtensorMap* map, const TensorDesc& t, int rows) {
-  return encode(map, t.ptr, t.D, {t.N, t.H, t.B}, {t.sN, t.sH, t.sB}, {rows, 1, 1});
+bool encode_keys_map(CUtensorMap* map, const TensorDesc& t, int rows) {
+  return encode_map(map, t.ptr, t.D, {t.N, t.H, t.B}, {t.sN, t.sH, t.sB}, {rows, 1, 1});
 }
 
-template <int D>
-cudaError_t launch(const CacheAttnParams& p, const AttnParts& parts, bool prefix, cudaStream_t s) {
-  const TensorDesc& K = prefix ? p.Kp : p.K;
-  const TensorDesc& V = prefix ? p.Vp : p.V;
-  const int G = static_cast<int>(p.Q.H / p.K.H);
-  const WideRows wr = wide_rows(p.Q.B, p.Q.N, G, prefix);
-  WideMaps maps;
-  if (!encode(&maps.q, p.Q.ptr, D, {p.Q.H, p.Q.N, p.Q.B}, {p.Q.sH, p.Q.sN, p.Q.sB},
-              {G, wr.pos_per_tile, wr.seqs_per_tile}) ||
-      !encode_keys(&maps.k, K, 128) || !encode_keys(&maps.v, V, 128) || !encode_keys(&maps.k16, K, 16) ||
-      !encode_keys(&maps.v16, V, 16))
-    return cudaErrorNotSupported;
-  cudaError_t e = cudaFuncSetAttribute(attn_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       WideCfg<D>::kBytes);
-  if (e != cudaSuccess) return e;
-  const int64_t ctas = wide_units(p.Q, p.K, prefix) * (prefix ? parts.prefix : parts.own);
-  attn_wide_kernel<D><<<static_cast<unsigned>(ctas), kThreads, WideCfg<D>::kBytes, s>>>(p, parts, prefix, wr, maps);
-  return cudaGetLastError();
+bool encode_queries_map(CUtensorMap* map, const TensorDesc& t, int heads, int positions, int seqs) {
+  return encode_map(map, t.ptr, t.D, {t.H, t.N, t.B}, {t.sH, t.sN, t.sB}, {heads, positions, seqs});
 }
-
-}  // namespace
 
 int64_t wide_units(const TensorDesc& Q, const TensorDesc& K, bool prefix) {
   const WideRows w = wide_rows(Q.B, Q.N, Q.H / K.H, prefix);

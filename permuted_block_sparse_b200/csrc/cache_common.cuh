@@ -46,6 +46,15 @@ __device__ __forceinline__ KeyRun key_run(int first, int last, int64_t window, i
   return k;
 }
 
+// Tensor maps with 128-byte swizzle for tma_rows_4d, 64 columns a box, rows and
+// sequences outside the tensor read as zeros.  Queries: coordinates (column,
+// head, row, sequence), so a box's rows in shared memory are (sequence, row,
+// head) with the head innermost.  Keys: coordinates (column, key, head,
+// sequence); broadcast (zero-stride) heads or sequences have extent 1.
+// (cache_attn_wide.cu)
+bool encode_queries_map(CUtensorMap* map, const TensorDesc& t, int heads, int rows, int seqs);
+bool encode_keys_map(CUtensorMap* map, const TensorDesc& t, int rows);
+
 // Either bf16 of a pair is NaN or infinite.
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;

@@ -1,59 +1,454 @@
 // pbs_key_mass: attention weight per key,
 //   mass[j] = decay prev[j] + sum over rows r that see j of 2^(x_rj - y_r),
 // x_rj = scale log2(e) Q[r].K[j], y_r = log2(e) lse[r], over the query rows of
-// all heads of a KV head.  fp32 products, the sum in fp64.
+// all heads of a KV head.  Products and exponentials in fp32; the weights of up
+// to 128 rows are added in fp32, those sums in fp64 (a prompt adds tens of
+// thousands of small terms to one key).  No atomics: a key's sum has one owner,
+// or parts that a second kernel adds in order.
+//
+// The keys are the rows of the MMA in both kernels (S^T = K Q^T), so that a
+// thread's values belong to one key and are summed in registers.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache_common.cuh"
+#include "mma_sync.cuh"
 
 namespace pbs {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// One thread per key; the query rows pass by in shared memory.
-__global__ void __launch_bounds__(kThreads) key_mass_row_kernel(KeyMassParams p) {
-  __shared__ float q[8][128];
-  const int tid = threadIdx.x, D = static_cast<int>(p.Q.D), G = static_cast<int>(p.Q.H / p.K.H);
-  const int64_t M = p.Q.N, N = p.K.N, b = blockIdx.y / p.K.H, hk = blockIdx.y % p.K.H;
-  const int64_t L = cache_len(p.mask.kv_len, b, N, p.err), n_rows = cache_len(p.mask.q_len, b, M, p.err);
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kThreads + tid;
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + hk * p.K.sH + j * p.K.sN;
-  double sum = 0.0;
-  for (int64_t i0 = 0; i0 < n_rows * G; i0 += 8) {
-    __syncthreads();
-    for (int i = tid; i < 8 * D; i += kThreads) {
-      const int64_t row = i0 + i / D;
-      if (row < n_rows * G)
-        q[i / D][i % D] = __bfloat162float(static_cast<const __nv_bfloat16*>(
-            p.Q.ptr)[b * p.Q.sB + (hk * G + row % G) * p.Q.sH + row / G * p.Q.sN + i % D]);
+// What is written for key j of row `bh` of the outputs, given its sum.
+__device__ __forceinline__ void write_mass(const KeyMassParams& p, int64_t bh, int64_t j, int L, double sum) {
+  float x = 0.f;
+  if (j < L) x = static_cast<float>(p.prev ? static_cast<double>(p.decay) * p.prev[bh * p.prev_stride + j] + sum : sum);
+  p.mass[bh * p.mass_stride + j] = x;
+}
+
+// ------------------------------------------------------------------ few rows
+// Up to 16 query rows per KV head (a decode step).  Four warps per CTA; each
+// warp streams groups of 16 keys through a private cp.async ring and multiplies
+// them as the A operand of m16n8k16 (keys x rows); the queries stay in registers
+// as the B operand.  A CTA's rounds of 64 keys are spread over the cache, so
+// that the keys outside a window, which are not loaded, fall on all CTAs alike.
+// Bound: HBM, 2 D bytes per visible key.
+constexpr int kWarps = 4;
+constexpr int kStages = 6;
+constexpr int kGroup = 16;
+
+template <int D, int NG>
+__global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassParams p, const int n_parts) {
+  constexpr int kTile = kGroup * D * 2;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int M = static_cast<int>(p.Q.N), N = static_cast<int>(p.K.N), Hq = static_cast<int>(p.Q.H);
+  const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
+  const int part = static_cast<int>(blockIdx.x) % n_parts, bh = static_cast<int>(blockIdx.x) / n_parts;
+  const int b = bh / Hkv, hk = bh % Hkv;
+  const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
+  const int64_t window = p.mask.window;
+  const int n_sink = p.mask.n_sink;
+  const int first = L - nq;                       // position of row 0
+  // keys that some row sees: j < n_sink or j >= lo_min (and j < L); keys that every row sees end at `first`
+  const int lo_min = static_cast<int>(max(static_cast<int64_t>(0), first - window + 1));
+  const int lo_max = static_cast<int>(max(static_cast<int64_t>(0), L - window));
+  const int seen_end = nq > 0 ? L : 0;
+
+  uint32_t qb[NG][D / 16][2];                     // Q as B fragments: row lane / 4 of each eight
+  float y[NG][2];                                 // and the lse of rows 2 (lane mod 4) + {0, 1}
+  int pos[NG][2];                                 // their positions; -1: no query
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int i = g * 8 + lane / 4;
+    const bool valid = i < nq * G;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q.ptr);
+    if (valid) q += b * p.Q.sB + (hk * G + i % G) * p.Q.sH + i / G * p.Q.sN + (lane & 3) * 2;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      qb[g][k][0] = valid ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
+      qb[g][k][1] = valid ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
     }
-    __syncthreads();
-    if (j >= L) continue;
-    for (int i = 0; i < 8 && i0 + i < n_rows * G; ++i) {
-      const int64_t r = (i0 + i) / G, h = hk * G + (i0 + i) % G;
-      const int64_t pos = L - n_rows + r;
-      if (j > pos || (j <= pos - p.mask.window && j >= p.mask.n_sink)) continue;
-      const float y = p.lse[(b * p.Q.H + h) * M + r];
-      if (y == -INFINITY) continue;
-      float s = 0.f;
-      for (int c = 0; c < D; ++c) s = fmaf(q[i][c], __bfloat162float(k[c]), s);
-      sum += exp2f(fmaf(s, p.scale_log2, -y * 1.4426950408889634f));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = g * 8 + (lane & 3) * 2 + e;
+      y[g][e] = INFINITY;                         // no query: weight 0
+      pos[g][e] = -1;
+      if (c < nq * G) {
+        const float x = p.lse[(static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + c / G];
+        if (x != -INFINITY) {
+          y[g][e] = x * kLog2e;
+          pos[g][e] = first + c / G;
+        }
+      }
     }
   }
+  const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + hk * p.K.sH;
+  const uint32_t ring = smem_u32(smem + warp * kStages * kTile);
+  constexpr int CH = D / 8, RPI = 32 / CH;
+  const int lc = lane % CH, lr = lane / CH;
+  auto base = [&](int i) { return ((static_cast<int64_t>(i) * n_parts + part) * kWarps + warp) * kGroup; };
+  auto some = [&](int64_t j0) { return j0 < seen_end && (j0 + kGroup > lo_min || j0 < n_sink); };
+  auto load = [&](int i, int st) {
+    const int64_t j0 = base(i);
+    if (some(j0)) {
+#pragma unroll
+      for (int it = 0; it < kGroup / RPI; ++it) {
+        const int r = it * RPI + lr;
+        const int64_t j = j0 + r;
+        const bool ok = j < L && (j >= lo_min || j < n_sink);
+        cp_async16_zfill(ring + st * kTile + rows_offset<D>(r, lc), kb + (ok ? j : 0) * p.K.sN + lc * 8, ok);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i, i);
+  int st = 0;
+  for (int i = 0; base(i) < N; ++i) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    load(i + kStages - 1, st == 0 ? kStages - 1 : st - 1);
+    const int64_t j0 = base(i);
+    const uint32_t sk = ring + st * kTile;
+    st = st == kStages - 1 ? 0 : st + 1;
+    float sum[2] = {0.f, 0.f};                    // keys lane / 4 and 8 + lane / 4
+    if (some(j0)) {
+      float s[NG][4];
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        // matrices: keys 0-7 | 8-15 | 0-7 | 8-15, chunks 2k | 2k | 2k+1 | 2k+1
+        uint32_t f[4];
+        ldsm4(f, sk + rows_offset<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * k + (lane >> 4)));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) mma_16816(s[g], f[0], f[1], f[2], f[3], qb[g][k][0], qb[g][k][1]);
+      }
+      const bool full = j0 + kGroup - 1 <= first && j0 + kGroup <= L && (j0 >= lo_max || j0 + kGroup <= n_sink);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float w = ex2(fmaf(s[g][e], p.scale_log2, -y[g][e & 1]));
+          if (!full) {
+            const int64_t j = j0 + (e >> 1) * 8 + lane / 4;
+            const int at = pos[g][e & 1];
+            if (j > at || (j <= at - window && j >= n_sink)) w = 0.f;
+          }
+          sum[e >> 1] += w;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+      }
+    }
+    if ((lane & 3) < 2) {
+      const int64_t j = j0 + (lane & 3) * 8 + lane / 4;
+      if (j < N) write_mass(p, bh, j, L, (lane & 3) ? sum[1] : sum[0]);
+    }
+  }
+  cp_async_wait_all();
+}
+
+// ------------------------------------------------------------------ many rows
+// One CTA per (128 keys, KV head, sequence, part of the query rows), the heaviest
+// key tiles (the first, which the most rows see) first.  The key tile stays in
+// shared memory as the A operand; the query rows stream past in TMA boxes packed
+// as (position, head of the group), up to 128 a box, as the B operand.
+//   warp 0  issues S^T = K Q^T into two tensor-memory buffers;
+//   warp 1  loads K once and the query boxes with their lse into a two-stage ring;
+//   warps 2-5 (one key per thread) take 2^(x - y) of every column and sum it.
+// Two CTAs per SM (96 KB and 256 tensor-memory columns each), so that one's
+// set-up hides behind the other.  Bound: exponentials, 16 per clock and SM.
+constexpr int kWideThreads = 192;
+constexpr int kQStages = 2;
+
+template <int D>
+struct MassCfg {
+  static constexpr int kTile = (D / 64) * 128 * 128;
+  static constexpr int kBytes = (1 + kQStages) * kTile + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMassParams p, const int n_parts,
+                                                                    const int pm, double* __restrict__ partial,
+                                                                    const __grid_constant__ CUtensorMap mq,
+                                                                    const __grid_constant__ CUtensorMap mk) {
+  using C = MassCfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bar_k, bar_q[kQStages], bar_qempty[kQStages], bar_s[2], bar_sfree[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_sh;
+  __shared__ __align__(16) float ny[kQStages][128];   // -log2(e) lse of the box's rows
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int M = static_cast<int>(p.Q.N), N = static_cast<int>(p.K.N), Hq = static_cast<int>(p.Q.H);
+  const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv, BH = static_cast<int>(p.K.B) * Hkv;
+  const int part = static_cast<int>(blockIdx.x) % n_parts, rest = static_cast<int>(blockIdx.x) / n_parts;
+  const int bh = rest % BH, j0 = rest / BH * 128, b = bh / Hkv, hk = bh % Hkv;
+  const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
+  const int64_t window = p.mask.window, first = L - nq;
+  const int n_sink = p.mask.n_sink;
+  // query rows that see some key of this tile: r0 <= r < r1, then this part's boxes of pm positions
+  const int64_t last_key = min(j0 + 127, L - 1);
+  int64_t r0 = max(static_cast<int64_t>(0), j0 - first), r1 = nq;
+  if (j0 >= n_sink) r1 = min(r1, last_key + window - first);
+  if (j0 >= L || r1 <= r0) r0 = r1 = 0;
+  const int n_box = static_cast<int>((r1 - r0 + pm - 1) / pm);
+  const int x0 = static_cast<int>(static_cast<int64_t>(n_box) * part / n_parts);
+  const int x1 = static_cast<int>(static_cast<int64_t>(n_box) * (part + 1) / n_parts);
+  const int cols = pm * G, n_mma = (cols + 15) / 16 * 16;
+  double* mine = n_parts > 1 ? partial + (static_cast<int64_t>(part) * BH + bh) * N : nullptr;
+  if (x0 == x1) {                                 // nothing sees these keys here
+    if (tid < 128 && j0 + tid < N) {
+      if (mine) mine[j0 + tid] = 0.0;
+      else write_mass(p, bh, j0 + tid, L, 0.0);
+    }
+    return;
+  }
+
+  const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + C::kTile);
+  // MMA columns past the box: zero rows (the boxes never write them)
+  for (int i = tid; i < kQStages * (n_mma - cols) * (D / 8); i += kWideThreads) {
+    const int c = i % (D / 8), r = cols + i / (D / 8) % (n_mma - cols), s = i / (D / 8) / (n_mma - cols);
+    *reinterpret_cast<uint4*>(smem + (1 + s) * C::kTile + (c / 8) * (128 * 128) + sw128_offset(r, c % 8)) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async();
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, 256);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    abort_sh = 0;
+    mbar_init(&bar_k, 1);
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(&bar_q[i], 33);                   // the box's bytes, and each lane's lse
+      mbar_init(&bar_qempty[i], 5);               // the MMAs, and the consumer warps' use of the lse
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_sfree[i], 4);
+    }
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  volatile int* abort_flag = &abort_sh;
+
+  if (warp == 1) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      mbar_expect_tx(&bar_k, C::kTile);
+      for (int c = 0; c < D / 64; ++c)
+        tma_rows_4d(sK + c * (128 * 128), &mk, c * 64, j0, p.K.sH == 0 ? 0 : hk, p.K.sB == 0 ? 0 : b, &bar_k);
+    }
+    auto lse_of = [&](int x, float (&v)[4]) {     // this lane's rows lane, lane + 32, ... of box x
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = lane + 32 * e;
+        const int64_t r = r0 + static_cast<int64_t>(x) * pm + c / G;
+        const float l = c < cols && r < nq ? p.lse[(static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + r] : -INFINITY;
+        v[e] = l == -INFINITY ? -INFINITY : -l * kLog2e;    // -inf: the row adds nothing
+      }
+    };
+    float v[4];
+    lse_of(x0, v);
+    int issued = x0;
+    bool ok = true;
+    for (int x = x0; ok && x < x1; ++x) {
+      const int i = x - x0, s = i % kQStages;
+      if (i >= kQStages)
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_or_abort(&bar_qempty[s], ((i / kQStages) - 1) & 1, p.err, abort_flag));
+      if (!ok) break;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ny[s][lane + 32 * e] = v[e];
+      if (lane == 0) {
+        mbar_expect_tx(&bar_q[s], static_cast<uint32_t>(cols * D * 2));
+        for (int c = 0; c < D / 64; ++c)
+          tma_rows_4d(sQ + s * C::kTile + c * (128 * 128), &mq, c * 64, hk * G, static_cast<int>(r0 + x * pm), b,
+                      &bar_q[s]);
+      }
+      mbar_arrive(&bar_q[s]);
+      issued = x + 1;
+      if (x + 1 < x1) lse_of(x + 1, v);
+    }
+    // no copy may be in flight when the CTA ends; without an abort the other
+    // roles have waited for all of them
+    if (*abort_flag) {
+      mbar_wait(&bar_k, 0, p.err);
+      for (int x = max(x0, issued - kQStages); x < issued; ++x)
+        mbar_wait(&bar_q[(x - x0) % kQStages], ((x - x0) / kQStages) & 1, p.err);
+    }
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- MMA
+    const uint32_t idesc = idesc_bf16(128, n_mma, false);
+    bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bar_k, 0, p.err, abort_flag));
+    for (int x = x0; ok && x < x1; ++x) {
+      const int i = x - x0, s = i % kQStages, d = i & 1;
+      ok = mbar_wait_or_abort(&bar_q[s], (i / kQStages) & 1, p.err, abort_flag);
+      if (ok && i >= 2) ok = mbar_wait_or_abort(&bar_sfree[d], ((i / 2) - 1) & 1, p.err, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t a0 = sdesc_sw128(sK, 16, 1024), b0 = sdesc_sw128(sQ + s * C::kTile, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * (128 * 128) + (kk % 4) * 32;
+        if (elect_one()) mma_ss(tmem + d * 128, sdesc_add(a0, off), sdesc_add(b0, off), idesc, kk > 0 ? 1u : 0u);
+      }
+      if (elect_one()) {
+        tc_commit(&bar_s[d]);
+        tc_commit(&bar_qempty[s]);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ----------------------------------------------------------- consumers
+    const int key = (warp & 3) * 32 + lane;       // tensor-memory lane
+    const int64_t j = j0 + key;
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    double sum = 0.0;
+    for (int x = x0; x < x1; ++x) {
+      const int i = x - x0, s = i % kQStages, d = i & 1;
+      // (after an abort the waits return at once; the sums are then meaningless
+      // and the error word says so)
+      mbar_wait_or_abort(&bar_q[s], (i / kQStages) & 1, p.err, abort_flag);
+      mbar_wait_or_abort(&bar_s[d], (i / 2) & 1, p.err, abort_flag);
+      tc_fence_after();
+      // rows of the box that see this key: c_lo <= c < c_hi
+      const int64_t row = r0 + static_cast<int64_t>(x) * pm, at = first + row;
+      const int64_t hi = j < n_sink ? nq - row : min(nq - row, j + window - at);
+      const int c_lo = static_cast<int>(min(static_cast<int64_t>(pm), max(static_cast<int64_t>(0), j - at))) * G;
+      const int c_hi = j < L ? static_cast<int>(min(static_cast<int64_t>(pm), max(static_cast<int64_t>(0), hi))) * G : 0;
+      const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == cols);
+      unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+      for (int c = 0; c < n_mma; c += 32) {
+        uint32_t u[32];
+        tmem_ld32(tS + d * 128 + c, u);
+        if (!full) {
+          const int lo = c_lo - c, up = c_hi - c;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e < lo || e >= up) u[e] = __float_as_uint(-INFINITY);
+        } else if (c + 32 > n_mma) {              // (the last 16 columns of the buffer hold nothing)
+#pragma unroll
+          for (int e = 16; e < 32; ++e) u[e] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(&ny[s][c + e]);
+          float t0, t1, t2, t3;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), sc2, n2.x), t0, t1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])), sc2, n2.y), t2, t3);
+          a2[(e / 2) & 3] = f2_add(a2[(e / 2) & 3], f2_pack(ex2(t0), ex2(t1)));
+          a2[(e / 2 + 1) & 3] = f2_add(a2[(e / 2 + 1) & 3], f2_pack(ex2(t2), ex2(t3)));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar_sfree[d]);
+        mbar_arrive(&bar_qempty[s]);
+      }
+      float s0, s1, s2, s3, s4, s5, s6, s7;
+      f2_unpack(a2[0], s0, s1);
+      f2_unpack(a2[1], s2, s3);
+      f2_unpack(a2[2], s4, s5);
+      f2_unpack(a2[3], s6, s7);
+      sum += static_cast<double>(((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7)));
+    }
+    if (j < N) {
+      if (mine) mine[j] = sum;
+      else write_mass(p, bh, j, L, sum);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+__global__ void __launch_bounds__(256) mass_join_kernel(const KeyMassParams p, const int n_parts,
+                                                        const double* __restrict__ partial) {
+  const int64_t N = p.K.N, BH = p.K.B * p.K.H, bh = blockIdx.y;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (j >= N) return;
-  const float old = p.prev && j < L ? p.decay * p.prev[blockIdx.y * p.prev_stride + j] : 0.f;
-  p.mass[blockIdx.y * p.mass_stride + j] = old + static_cast<float>(sum);
+  double sum = 0.0;
+  for (int s = 0; s < n_parts; ++s) sum += partial[(s * BH + bh) * N + j];
+  write_mass(p, bh, j, cache_len(p.mask.kv_len, bh / p.K.H, N, p.err), sum);
+}
+
+constexpr int kFewRows = 16;
+constexpr int kMaxParts = 8;
+
+// Parts that the query rows are cut into: enough for four CTAs per SM, at least
+// four boxes each.  More parts than that only add partial sums.
+int mass_parts(const TensorDesc& Q, const TensorDesc& K) {
+  const int64_t G = Q.H / K.H, tiles = (K.N + 127) / 128 * K.B * K.H;
+  if (Q.N * G <= kFewRows) return 1;
+  const int64_t boxes = (Q.N * G + 127) / 128;
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min({boxes / 4, 4 * kSMs / tiles, static_cast<int64_t>(kMaxParts)})));
+}
+
+template <int D>
+cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
+  const int64_t G = p.Q.H / p.K.H, rows = p.Q.N * G, BH = p.K.B * p.K.H;
+  if (rows <= kFewRows) {
+    const int64_t rounds = (p.K.N + kWarps * kGroup - 1) / (kWarps * kGroup);
+    // two CTAs per SM, and no more than there are rounds
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds, (8 * kSMs + BH - 1) / BH)));
+    const int bytes = kWarps * kStages * kGroup * D * 2;
+    auto kernel = rows <= 8 ? mass_few_kernel<D, 1> : mass_few_kernel<D, 2>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(BH * parts), kWarps * 32, bytes, s>>>(p, parts);
+    return cudaGetLastError();
+  }
+  const int pm = static_cast<int>(std::min(p.Q.N, 128 / G));
+  const int parts = mass_parts(p.Q, p.K);
+  CUtensorMap mq, mk;
+  if (!encode_queries_map(&mq, p.Q, static_cast<int>(G), pm, 1) || !encode_keys_map(&mk, p.K, 128))
+    return cudaErrorNotSupported;
+  cudaError_t e = cudaFuncSetAttribute(mass_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       MassCfg<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = (p.K.N + 127) / 128 * BH * parts;
+  if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
+  double* partial = static_cast<double*>(p.ws);
+  mass_wide_kernel<D><<<static_cast<unsigned>(ctas), kWideThreads, MassCfg<D>::kBytes, s>>>(p, parts, pm, partial, mq,
+                                                                                           mk);
+  if ((e = cudaGetLastError()) != cudaSuccess || parts == 1) return e;
+  mass_join_kernel<<<dim3(static_cast<unsigned>((p.K.N + 255) / 256), static_cast<unsigned>(BH)), 256, 0, s>>>(p, parts,
+                                                                                                           partial);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t key_mass_ws_bytes(const TensorDesc&, const TensorDesc&) { return 0; }
+size_t key_mass_ws_bytes(const TensorDesc& Q, const TensorDesc& K) {
+  if (K.H > Q.H || Q.H % K.H) return 0;
+  const int parts = mass_parts(Q, K);
+  return parts == 1 ? 0 : static_cast<size_t>(parts) * K.B * K.H * K.N * sizeof(double);
+}
 
 cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.K.N + kThreads - 1) / kThreads), static_cast<unsigned>(p.K.B * p.K.H));
-  key_mass_row_kernel<<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.Q.D == 128 ? launch<128>(p, s) : launch<64>(p, s);
 }
 
 }  // namespace pbs
