@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -380,21 +381,43 @@ def pbs_attn_fwd_early_stop(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, p
 
 
 # --------------------------------------------------------- cache operators
+# Stream handle of a device's current stream; the private function is the one
+# torch's own code generators launch by, 3 us cheaper than a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _place(stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
     """Context in which a cache operator allocates and launches: the tensors'
     device, and ``stream`` where one is given, so that what is allocated here
     belongs to the stream that uses it."""
-    dev = first.device
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        if stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
         return torch.cuda.stream(stream)
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+    if dev >= 0 and dev != torch.cuda.current_device():
         return torch.cuda.device(dev)
     return _HERE_AND_NOW
+
+
+@functools.lru_cache(maxsize=512)
+def _cache_ws_bytes(op: int, B: int, Hq: int, M: int, D: int, Hkv: int, N: int) -> int:
+    q = PbsTensor(256, B, Hq, M, D, Hq * M * D, M * D, D)        # only the shapes are read
+    k = PbsTensor(256, B, Hkv, N, D, Hkv * N * D, N * D, D)
+    return load().pbs_workspace_size(op, q, k, 0, 0)
+
+
+def _cache_ws(ws: Optional[torch.Tensor], nbytes: int, like: torch.Tensor):
+    """(owner, address, bytes) of the caller's workspace or a new one."""
+    if ws is None:
+        if nbytes == 0:
+            return None, None, 0
+        ws = like.new_empty(nbytes + 256, dtype=torch.uint8)
+    return ws, *_aligned(ws)
 
 
 def _lengths(name: str, t: Optional[torch.Tensor], B: int) -> Optional[int]:
@@ -432,7 +455,7 @@ def _check_out(name: str, t: torch.Tensor, dtype, shape: Tuple[int, ...]) -> Non
 
 
 def _cache_attn(Q, Kp, Vp, K, V, window, n_sink, kv_len, q_len, softmax_scale, out, lse, want_lse, ws, stream):
-    lib = load()
+    lib = _lib or load()
     q, k, v = describe(Q), describe(K), describe(V)
     B, Hq, M, D = Q.shape
     kv, ql = _lengths("kv_len", kv_len, B), _lengths("q_len", q_len, B)
@@ -441,16 +464,14 @@ def _cache_attn(Q, Kp, Vp, K, V, window, n_sink, kv_len, q_len, softmax_scale, o
         softmax_scale = 1.0 / math.sqrt(D)
     with _place(stream, Q, K, V, Kp, Vp, kv_len, q_len, out, lse, ws):
         if out is None:
-            out = torch.empty((B, Hq, M, D), dtype=torch.bfloat16, device=Q.device)
+            out = torch.empty_like(Q)
         if lse is not None:
             _check_out("lse", lse, torch.float32, (B, Hq, M))
         elif want_lse:
-            lse = torch.empty((B, Hq, M), dtype=torch.float32, device=Q.device)
-        if ws is None:
-            op = PBS_OP_ATTN_WINDOW if Kp is None else PBS_OP_ATTN_PREFIX
-            ws = _workspace(lib.pbs_workspace_size(op, q, k, 0, 0), Q.device)
-        wp, wn = _aligned(ws)
-        o, s = describe(out), _stream(stream)
+            lse = Q.new_empty((B, Hq, M), dtype=torch.float32)
+        op = PBS_OP_ATTN_WINDOW if Kp is None else PBS_OP_ATTN_PREFIX
+        ws, wp, wn = _cache_ws(ws, _cache_ws_bytes(op, B, Hq, M, D, k.H, k.N), Q)
+        o, s = describe(out), _raw_stream(Q.get_device())
         if Kp is None:
             rc = lib.pbs_attn_window(q, k, v, kv, ql, window, n_sink, softmax_scale, o, _ptr(lse), wp, wn, s)
         else:
@@ -495,10 +516,10 @@ def pbs_key_mass(Q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, mass: Opti
     """[B, Hkv, N] fp32: ``decay`` times the earlier ``mass`` (None: zero) plus
     the attention weight that the rows of ``Q`` give each key, from the ``lse``
     of their attention.  ``out`` may be ``mass`` itself."""
-    lib = load()
+    lib = _lib or load()
     q, k = describe(Q), describe(K)
     B, Hq, M, D = Q.shape
-    shape = (B, K.shape[1], K.shape[2])
+    shape = (B, k.H, k.N)
     kv, ql = _lengths("kv_len", kv_len, B), _lengths("q_len", q_len, B)
     _int32("n_sink", n_sink)
     _check_out("lse", lse, torch.float32, (B, Hq, M))
@@ -507,13 +528,11 @@ def pbs_key_mass(Q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, mass: Opti
     s_in = 0 if mass is None else _row_stride("mass", mass, shape)
     with _place(stream, Q, K, lse, mass, kv_len, q_len, out, ws):
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=Q.device)
+            out = Q.new_empty(shape, dtype=torch.float32)
         s_out = _row_stride("out", out, shape)
-        if ws is None:
-            ws = _workspace(lib.pbs_workspace_size(PBS_OP_KEY_MASS, q, k, 0, 0), Q.device)
-        wp, wn = _aligned(ws)
+        ws, wp, wn = _cache_ws(ws, _cache_ws_bytes(PBS_OP_KEY_MASS, B, Hq, M, D, k.H, k.N), Q)
         rc = lib.pbs_key_mass(q, k, lse.data_ptr(), kv, ql, window, n_sink, decay, softmax_scale, _ptr(mass), s_in,
-                              out.data_ptr(), s_out, wp, wn, _stream(stream))
+                              out.data_ptr(), s_out, wp, wn, _raw_stream(Q.get_device()))
     _check(rc)
     return out
 
@@ -528,7 +547,7 @@ def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int,
     last ``recent`` always stay and the rest are those of highest ``mass``.
     ``K_out`` and ``V_out`` [B, Hkv, n >= budget, D] and ``mass_out``
     [B, Hkv, n >= budget] take the kept rows at their start."""
-    lib = load()
+    lib = _lib or load()
     k, v = describe(K), describe(V)
     B, Hkv, N, D = K.shape
     kv = _lengths("kv_len", kv_len, B)
@@ -537,30 +556,27 @@ def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int,
         raise ValueError(f"budget {budget} is not in [1, N = {N}]")
     _int32("recent", recent), _int32("n_sink", n_sink)
     with _place(stream, K, V, mass, kv_len, keep, K_out, V_out, mass_out, new_len, ws):
-        dev = K.device
         if keep is None:
-            keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev)
+            keep = K.new_empty((B, Hkv, budget), dtype=torch.int32)
         else:
             _check_out("keep", keep, torch.int32, (B, Hkv, budget))
         if K_out is None:
-            K_out = torch.empty((B, Hkv, budget, D), dtype=torch.bfloat16, device=dev)
+            K_out = K.new_empty((B, Hkv, budget, D))
         if V_out is None:
-            V_out = torch.empty((B, Hkv, K_out.shape[2], D), dtype=torch.bfloat16, device=dev)
+            V_out = K.new_empty((B, Hkv, K_out.shape[2], D))
         if mass_out is None:
-            mass_out = torch.empty((B, Hkv, budget), dtype=torch.float32, device=dev)
+            mass_out = mass.new_empty((B, Hkv, budget))
         s_out = _row_stride("mass_out", mass_out, (B, Hkv) + tuple(mass_out.shape[2:]))
         if mass_out.shape[2] < budget:
             raise ValueError(f"mass_out has room for {mass_out.shape[2]} of {budget} keys")
         if new_len is None:
-            new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+            new_len = K.new_empty((B,), dtype=torch.int32)
         else:
             _check_out("new_len", new_len, torch.int32, (B,))
-        if ws is None:
-            ws = _workspace(lib.pbs_workspace_size(PBS_OP_EVICT, k, k, 0, 0), dev)
-        wp, wn = _aligned(ws)
+        ws, wp, wn = _cache_ws(ws, _cache_ws_bytes(PBS_OP_EVICT, B, Hkv, N, D, Hkv, N), K)
         rc = lib.pbs_evict(mass.data_ptr(), s_in, k, v, kv, budget, recent, n_sink, keep.data_ptr(),
                            new_len.data_ptr(), describe(K_out), describe(V_out), mass_out.data_ptr(), s_out, wp, wn,
-                           _stream(stream))
+                           _raw_stream(K.get_device()))
     _check(rc)
     return keep, K_out, V_out, mass_out, new_len
 

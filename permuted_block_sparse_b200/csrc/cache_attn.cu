@@ -4,8 +4,9 @@
 //   m_r = max_j x_rj,  l_r = sum_j 2^(x_rj - m_r),  lse_r = ln 2 (m_r + log2 l_r)
 //
 // over the keys j that row r sees, in one pass with the running (m, l, O)
-// rescaled whenever m grows.  The key axis may be cut into parts that different
-// CTAs run; a part leaves its (m, l, O) in fp32 and attn_join_kernel adds them.
+// rescaled whenever m grows.  The key axis may be cut into parts: the CTAs of a
+// cluster join theirs through distributed shared memory; what several clusters
+// (or several CTAs of the tcgen05 kernel) leave in fp32, attn_join_kernel adds.
 //
 // Query rows of one KV head that read the same keys run together: the G heads
 // of the group, the M new tokens and, over a shared prefix, the sequences.  Up
@@ -36,6 +37,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kGroup = 16;                      // keys per warp and stage
+constexpr int kMaxRank = 8;                     // CTAs per cluster
 
 template <int D>
 struct FewCfg {
@@ -53,17 +55,20 @@ struct FewRow {
 // A group of keys that only some rows see and that holds NaN or infinities
 // among its values (rare): add those entries to the rows that do see them --
 // exp is never zero, so such an entry is what its column becomes -- and zero
-// them for the product.  Whole warp; col0 + 8 j + {0, 1} are a thread's columns.
+// them for the product.  Whole warp; 8 j + 2 (lane mod 4) + {0, 1} are a
+// thread's columns.  (Inline: out of line, `o` would live in local memory.)
 template <int D, int NG>
-__device__ __noinline__ void few_nonfinite(unsigned char* v, const FewRow* row, int n_sink, int v0, int lane,
+__device__ __forceinline__ void few_nonfinite(unsigned char* v, const FewRow* row, int n_sink, int v0, int lane,
                                            float (&o)[NG][D / 8][4]) {
+#pragma unroll
   for (int g = 0; g < NG; ++g) {
     const FewRow me = row[g * 8 + lane / 4];
+#pragma unroll 1
+    for (int k = 0; k < kGroup; ++k) {
+      const int i = v0 + k;
+      if (i > me.hi || (i < me.lo && i >= n_sink)) continue;
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      for (int k = 0; k < kGroup; ++k) {
-        const int i = v0 + k;
-        if (i > me.hi || (i < me.lo && i >= n_sink)) continue;
+      for (int j = 0; j < D / 8; ++j) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(v + rows_offset<D>(k, j) + (lane & 3) * 4);
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
         if (!isfinite(f.x)) o[g][j][0] += f.x;
@@ -79,18 +84,21 @@ __device__ __noinline__ void few_nonfinite(unsigned char* v, const FewRow* row, 
 
 template <int D, int NG>
 __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAttnParams p, const AttnParts parts,
-                                                                  const int prefix_ctas) {
+                                                                  const int prefix_ctas, const int n_rank) {
   using C = FewCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ FewRow row[NG * 8];
   __shared__ float sm_m[kWarps][NG * 8], sm_l[kWarps][NG * 8];
+  __shared__ float2 sm_ml[NG * 8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int M = static_cast<int>(p.Q.N), Hq = static_cast<int>(p.Q.H), Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
+
+  wait_for_previous_kernel();
 
   // this CTA's rows and keys
   const bool pre = static_cast<int>(blockIdx.x) < prefix_ctas;
   const int cta = pre ? blockIdx.x : blockIdx.x - prefix_ctas;
-  const int n_parts = pre ? parts.prefix : parts.own;
+  const int n_clusters = pre ? parts.prefix : parts.own, n_parts = n_clusters * n_rank;
   const int part = cta % n_parts, unit = cta / n_parts;
   const int hk = unit % Hkv, b = pre ? 0 : unit / Hkv;
   const int R = (pre ? static_cast<int>(p.Q.B) : 1) * M * G;
@@ -292,7 +300,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
     }
   }
   __syncthreads();
-  const int slot = pre ? part : parts.prefix + part, n_slots = parts.prefix + parts.own;
+  const int n_slots = parts.prefix + parts.own, slot = (pre ? 0 : parts.prefix) + part / n_rank;
   for (int id = tid; id < R * (D / 4); id += kWarps * 32) {
     const int i = id / (D / 4), c = id % (D / 4) * 4;
     if (row[i].out < 0) continue;
@@ -302,91 +310,168 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (sm_m[w][i] != -INFINITY || sm_l[w][i] != 0.f) ll += sm_l[w][i] * (mm == -INFINITY ? 1.f : ex2(sm_m[w][i] - mm));
+      if (sm_l[w][i] != 0.f) ll += sm_l[w][i] * (mm == -INFINITY ? 1.f : ex2(sm_m[w][i] - mm));
       const float4 x = *reinterpret_cast<const float4*>(so + (w * NG * 8 + i) * D + c);
       acc.x += x.x;
       acc.y += x.y;
       acc.z += x.z;
       acc.w += x.w;
     }
-    if (n_slots == 1) {
-      write_row4(p, row[i].out, c, acc, mm, ll);
+    if (n_rank == 1) {
+      leave_row4(p, parts, n_slots, slot, row[i].out, c, D, acc, mm, ll);
     } else {
-      const int64_t at = static_cast<int64_t>(row[i].out) * n_slots + slot;
-      if (ll != 0.f) *reinterpret_cast<float4*>(parts.acc + at * D + c) = acc;
-      if (c == 0) parts.ml[at] = make_float2(mm, ll);
+      *reinterpret_cast<float4*>(so + i * D + c) = acc;          // (this thread alone reads and writes it)
+      if (c == 0) sm_ml[i] = make_float2(mm, ll);
     }
   }
+  if (n_rank == 1) return;
+  // ---- join the cluster: each CTA takes every n_rank-th piece of the rows
+  cluster_sync_all();
+  const uint32_t so_s = smem_u32(so), ml_s = smem_u32(sm_ml);
+  for (int id = tid * n_rank + part % n_rank; id < R * (D / 4); id += kWarps * 32 * n_rank) {
+    const int i = id / (D / 4), c = id % (D / 4) * 4;
+    if (row[i].out < 0) continue;
+    float2 ml[kMaxRank];
+    float4 x[kMaxRank];
+#pragma unroll
+    for (int q = 0; q < kMaxRank; ++q) {
+      if (q >= n_rank) break;
+      ml[q] = ld_cluster_f2(mapa_shared(ml_s + i * 8, q));
+      x[q] = ld_cluster_f4(mapa_shared(so_s + (i * D + c) * 4, q));
+    }
+    float mm = -INFINITY, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < kMaxRank; ++q)
+      if (q < n_rank) mm = fmaxf(mm, ml[q].x);
+#pragma unroll
+    for (int q = 0; q < kMaxRank; ++q) {
+      if (q >= n_rank || ml[q].y == 0.f) continue;
+      const float w = mm == -INFINITY ? 1.f : ex2(ml[q].x - mm);
+      ll = fmaf(w, ml[q].y, ll);
+      acc.x = fmaf(w, x[q].x, acc.x);
+      acc.y = fmaf(w, x[q].y, acc.y);
+      acc.z = fmaf(w, x[q].z, acc.z);
+      acc.w = fmaf(w, x[q].w, acc.w);
+    }
+    leave_row4(p, parts, n_slots, slot, row[i].out, c, D, acc, mm, ll);
+  }
+  cluster_sync_all();                             // the others may still read this CTA's shared memory
 }
 
 // ---------------------------------------------------------------- joining
-// One warp per output row: the largest maximum, then the parts' sums and
-// accumulators rescaled to it, in the order of the parts.
+constexpr int kMaxParts = 32;      // that the prefix and the own keys each leave to attn_join_kernel
+// One warp per output row, lane s looking after part s, s + 32, ...: the largest
+// maximum, then the parts' sums and accumulators rescaled to it and added in the
+// order of the parts, eight accumulator rows in flight.
 template <int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const CacheAttnParams p, const AttnParts parts) {
+  wait_for_previous_kernel();
   const int64_t out = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, n = parts.prefix + parts.own;
   const int64_t M = p.Q.N;
   if (out >= p.Q.B * p.Q.H * M) return;
   if (p.mask.q_len && out % M >= cache_len(p.mask.q_len, out / M / p.Q.H, M, p.err)) return;
-  const float2* ml = parts.ml + out * n;
+  constexpr int E = D / 32, kHold = (2 * kMaxParts + 31) / 32;
+  float2 ml[kHold];
   float mm = -INFINITY;
-  for (int s = lane; s < n; s += 32) mm = fmaxf(mm, ml[s].x);
+#pragma unroll
+  for (int q = 0; q < kHold; ++q) {
+    ml[q] = lane + 32 * q < n ? parts.ml[out * n + lane + 32 * q] : make_float2(-INFINITY, 0.f);
+    mm = fmaxf(mm, ml[q].x);
+  }
   for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-  const float* acc = parts.acc + out * n * D + lane * (D / 32);
-  float ll = 0.f, a[D / 32];
+  const float* acc = parts.acc + out * n * D + lane * E;
+  float ll = 0.f, a[E];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) a[e] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const float2 x = ml[s];
-    if (x.y == 0.f) continue;                     // a part in which the row sees nothing
-    const float w = x.x == mm ? 1.f : ex2(x.x - mm);
-    ll += w * x.y;
+  for (int e = 0; e < E; ++e) a[e] = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) a[e] = fmaf(w, acc[static_cast<int64_t>(s) * D + e], a[e]);
+  for (int q = 0; q < kHold; ++q) {
+    if (q * 32 >= n) break;
+    // (a part in which the row sees nothing has sum 0 and no accumulator)
+    const float w = ml[q].y == 0.f ? 0.f : mm == -INFINITY ? 1.f : ex2(ml[q].x - mm);
+    const float wl = ml[q].y == 0.f ? 0.f : w * ml[q].y;
+    for (int s0 = 0; s0 < 32 && q * 32 + s0 < n; s0 += 8) {
+      float x[8][E];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const bool some = q * 32 + s0 + s < n && __shfl_sync(0xffffffffu, ml[q].y, s0 + s) != 0.f;
+        const float* at = acc + static_cast<int64_t>(q * 32 + s0 + s) * D;
+        if constexpr (E == 4) {
+          const float4 f = some ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[s][0] = f.x;
+          x[s][1] = f.y;
+          x[s][2] = f.z;
+          x[s][3] = f.w;
+        } else {
+          const float2 f = some ? *reinterpret_cast<const float2*>(at) : make_float2(0.f, 0.f);
+          x[s][0] = f.x;
+          x[s][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s0 + s);
+        ll += __shfl_sync(0xffffffffu, wl, s0 + s);
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = fmaf(ws, x[s][e], a[e]);
+      }
+    }
   }
   const float inv = ll == 0.f ? 0.f : 1.f / ll;
   const int64_t b = out / M / p.Q.H, h = out / M % p.Q.H, r = out % M;
   __nv_bfloat16* o =
-      static_cast<__nv_bfloat16*>(const_cast<void*>(p.O.ptr)) + b * p.O.sB + h * p.O.sH + r * p.O.sN + lane * (D / 32);
-#pragma unroll
-  for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
+      static_cast<__nv_bfloat16*>(const_cast<void*>(p.O.ptr)) + b * p.O.sB + h * p.O.sH + r * p.O.sN + lane * E;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(a[0] * inv, a[1] * inv);
   if (lane == 0 && p.lse) p.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
 }
 
 template <int D, int NG>
-cudaError_t run_few(const CacheAttnParams& p, const AttnParts& parts, int prefix_ctas, int own_ctas, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       FewCfg<D>::kBytes);
+cudaError_t run_few(const CacheAttnParams& p, const AttnParts& parts, int prefix_ctas, int ctas, int rank,
+                    cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(attn_few_kernel<D, NG>, FewCfg<D>::kBytes, done);
   if (e != cudaSuccess) return e;
-  attn_few_kernel<D, NG><<<prefix_ctas + own_ctas, kWarps * 32, FewCfg<D>::kBytes, s>>>(p, parts, prefix_ctas);
-  return cudaGetLastError();
+  return launch_after(attn_few_kernel<D, NG>, static_cast<unsigned>(ctas), kWarps * 32, FewCfg<D>::kBytes, rank, s, p,
+                      parts, prefix_ctas, rank);
 }
 
 constexpr int kFewRows = 16;
-constexpr int kMaxParts = 64;      // of the prefix and of the own keys each
+constexpr int kFewCtas = 4 * kSMs;
+constexpr int kFewKeys = 64;
 
 // Parts that `units` independent pieces of work of at most `keys` keys are cut
 // into: enough for `ctas` CTAs, none shorter than `shortest` keys.
-int cut(int64_t units, int64_t keys, int64_t ctas, int64_t shortest) {
-  const int64_t most = std::max<int64_t>(1, keys / shortest);
-  return static_cast<int>(std::max<int64_t>(1, std::min({most, ctas / units, static_cast<int64_t>(kMaxParts)})));
+int cut(int64_t units, int64_t keys, int64_t ctas, int64_t shortest, int64_t most) {
+  return static_cast<int>(std::max<int64_t>(1, std::min({keys / shortest, ctas / units, most})));
+}
+int power_of_two_up_to(int n) {
+  int x = 1;
+  while (2 * x <= n) x *= 2;
+  return x;
 }
 
 struct Plan {
   bool few_own, few_prefix;
-  int own, prefix;                 // parts
+  int rank;                        // CTAs per cluster of the few-row kernel
+  int own, prefix;                 // parts left to attn_join_kernel
 };
 Plan plan(const TensorDesc& Q, const TensorDesc& K, int64_t keys, bool has_prefix, int64_t P) {
   const int64_t G = Q.H / K.H, rows = Q.N * G;
   Plan w{};
   w.few_own = rows <= kFewRows;
-  w.own = w.few_own ? cut(K.B * K.H, keys, 4 * kSMs, 256) : cut(wide_units(Q, K, false), keys, kSMs, 256);
-  if (has_prefix) {
-    w.few_prefix = Q.B * rows <= kFewRows;
-    w.prefix = w.few_prefix ? cut(K.H, P, 2 * kSMs, 64) : cut(wide_units(Q, K, true), P, kSMs, 256);
-  }
+  w.few_prefix = has_prefix && Q.B * rows <= kFewRows;
+  w.rank = 1;
+  int own = 0, prefix = 0;
+  if (w.few_own) own = cut(K.B * K.H, keys, kFewCtas, kFewKeys, kMaxParts * kMaxRank);
+  if (w.few_prefix) prefix = cut(K.H, P, kFewCtas, kFewKeys, kMaxParts * kMaxRank);
+  w.rank = power_of_two_up_to(std::min(std::max({own, prefix, 1}), kMaxRank));
+  w.own = w.few_own ? std::max(own / w.rank, 1) : cut(wide_units(Q, K, false), keys, kSMs, 256, kMaxParts);
+  if (has_prefix)
+    w.prefix = w.few_prefix ? std::max(prefix / w.rank, 1) : cut(wide_units(Q, K, true), P, kSMs, 256, kMaxParts);
   return w;
 }
 
@@ -412,27 +497,18 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s) {
   parts.ml = reinterpret_cast<float2*>(parts.acc + rows * n * p.Q.D);
   const bool two = std::max(w.few_own ? p.Q.N * (p.Q.H / p.K.H) : 0,
                             w.few_prefix ? p.Q.B * p.Q.N * (p.Q.H / p.K.H) : 0) > 8;
-  const int prefix_ctas = w.few_prefix ? static_cast<int>(p.K.H) * w.prefix : 0;
-  const int own_ctas = w.few_own ? static_cast<int>(p.K.B * p.K.H) * w.own : 0;
+  const int prefix_ctas = w.few_prefix ? static_cast<int>(p.K.H) * w.prefix * w.rank : 0;
+  const int ctas = prefix_ctas + (w.few_own ? static_cast<int>(p.K.B * p.K.H) * w.own * w.rank : 0);
   cudaError_t e = cudaSuccess;
   if (pre && !w.few_prefix && (e = launch_attn_wide(p, parts, true, s)) != cudaSuccess) return e;
   if (!w.few_own && (e = launch_attn_wide(p, parts, false, s)) != cudaSuccess) return e;
-  if (prefix_ctas + own_ctas > 0) {
-    if (p.Q.D == 128)
-      e = two ? run_few<128, 2>(p, parts, prefix_ctas, own_ctas, s) : run_few<128, 1>(p, parts, prefix_ctas, own_ctas, s);
-    else
-      e = two ? run_few<64, 2>(p, parts, prefix_ctas, own_ctas, s) : run_few<64, 1>(p, parts, prefix_ctas, own_ctas, s);
-    if (e != cudaSuccess) return e;
+  if (ctas > 0) {
+    auto run = p.Q.D == 128 ? (two ? run_few<128, 2> : run_few<128, 1>) : (two ? run_few<64, 2> : run_few<64, 1>);
+    if ((e = run(p, parts, prefix_ctas, ctas, w.rank, s)) != cudaSuccess) return e;
   }
-  if (n > 1) {
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    if (p.Q.D == 128)
-      attn_join_kernel<128><<<grid, 128, 0, s>>>(p, parts);
-    else
-      attn_join_kernel<64><<<grid, 128, 0, s>>>(p, parts);
-    e = cudaGetLastError();
-  }
-  return e;
+  if (n == 1) return cudaSuccess;
+  return launch_after(p.Q.D == 128 ? attn_join_kernel<128> : attn_join_kernel<64>,
+                      static_cast<unsigned>((rows + 3) / 4), 128, 0, 1, s, p, parts);
 }
 
 }  // namespace pbs

@@ -26,6 +26,19 @@ __device__ __forceinline__ void write_row4(const CacheAttnParams& p, int64_t out
   if (c == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+// Four columns of one of n parts of output row `out`: the result itself where
+// there is one part.
+__device__ __forceinline__ void leave_row4(const CacheAttnParams& p, const AttnParts& parts, int n, int part,
+                                           int64_t out, int c, int D, float4 acc, float m, float l) {
+  if (n == 1) {
+    write_row4(p, out, c, acc, m, l);
+    return;
+  }
+  const int64_t at = out * n + part;
+  if (l != 0.f) *reinterpret_cast<float4*>(parts.acc + at * D + c) = acc;
+  if (c == 0) parts.ml[at] = make_float2(m, l);
+}
+
 // Pieces of work of the wide kernel before the keys are cut, and its launch
 // over the prefix or the own keys.
 int64_t wide_units(const TensorDesc& Q, const TensorDesc& K, bool prefix);

@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   const int M = static_cast<int>(p.Q.N), Hq = static_cast<int>(p.Q.H), Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
   const int B = static_cast<int>(p.Q.B);
 
+  wait_for_previous_kernel();
+
   // ---- this CTA's work: a pair of tiles, a KV head (and sequence), a part of the keys
   const int n_parts = prefix ? parts.prefix : parts.own;
   const int pairs = (wr.tiles + 1) / 2;
@@ -556,12 +558,12 @@ cudaError_t launch(const CacheAttnParams& p, const AttnParts& parts, bool prefix
       !encode_keys_map(&maps.k, K, 128) || !encode_keys_map(&maps.v, V, 128) || !encode_keys_map(&maps.k16, K, 16) ||
       !encode_keys_map(&maps.v16, V, 16))
     return cudaErrorNotSupported;
-  cudaError_t e = cudaFuncSetAttribute(attn_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       WideCfg<D>::kBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(attn_wide_kernel<D>, WideCfg<D>::kBytes, done);
   if (e != cudaSuccess) return e;
   const int64_t ctas = wide_units(p.Q, p.K, prefix) * (prefix ? parts.prefix : parts.own);
-  attn_wide_kernel<D><<<static_cast<unsigned>(ctas), kThreads, WideCfg<D>::kBytes, s>>>(p, parts, prefix, wr, maps);
-  return cudaGetLastError();
+  return launch_after(attn_wide_kernel<D>, static_cast<unsigned>(ctas), kThreads, WideCfg<D>::kBytes, 1, s, p, parts,
+                      prefix, wr, maps);
 }
 
 }  // namespace

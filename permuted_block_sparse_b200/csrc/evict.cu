@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   __shared__ uint32_t sh_digit, sh_need, wsum[kThreads / 32];
   __shared__ int above[kThreads / 32], equal[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  wait_for_previous_kernel();
   const int64_t row = blockIdx.x, b = row / p.K.H;
   const int L = cache_len(p.kv_len, b, p.K.N, p.err);
   const float* mass = p.mass + row * p.mass_stride;
@@ -135,8 +136,11 @@ constexpr int kGatherRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p) {
   constexpr int CH = D / 8, RP = 256 / CH;          // chunks a row, rows a pass of the CTA
-  const int64_t row = blockIdx.y, b = row / p.K.H, h = row % p.K.H;
-  const int c = threadIdx.x % CH * 8, i0 = static_cast<int>(blockIdx.x) * RP * kGatherRows + threadIdx.x / CH;
+  wait_for_previous_kernel();
+  const int blocks = (p.budget + RP * kGatherRows - 1) / (RP * kGatherRows);
+  const int64_t row = blockIdx.x / blocks, b = row / p.K.H, h = row % p.K.H;
+  const int c = threadIdx.x % CH * 8;
+  const int i0 = static_cast<int>(blockIdx.x) % blocks * RP * kGatherRows + threadIdx.x / CH;
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + h * p.K.sH + c;
   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.V.ptr) + b * p.V.sB + h * p.V.sH + c;
   __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(const_cast<void*>(p.Ko.ptr)) + b * p.Ko.sB + h * p.Ko.sH + c;
@@ -166,24 +170,21 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p) 
 size_t evict_ws_bytes(const TensorDesc&) { return 0; }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(p.K.B * p.K.H);
-  cudaError_t e = cudaSuccess;
-  if (p.K.N <= kHeldKeys) {
-    const int bytes = static_cast<int>(p.K.N) * 4;
-    e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldKeys * 4);
-    if (e != cudaSuccess) return e;
-    evict_select_kernel<true><<<rows, kThreads, bytes, s>>>(p);
-  } else {
-    evict_select_kernel<false><<<rows, kThreads, 0, s>>>(p);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t rows = p.K.B * p.K.H;
   const int per_cta = 256 / static_cast<int>(p.K.D / 8) * kGatherRows;
-  const dim3 grid(static_cast<unsigned>((p.budget + per_cta - 1) / per_cta), rows);
-  if (p.K.D == 128)
-    evict_gather_kernel<128><<<grid, 256, 0, s>>>(p);
-  else
-    evict_gather_kernel<64><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  const int64_t ctas = rows * ((p.budget + per_cta - 1) / per_cta);
+  if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
+  const bool held = p.K.N <= kHeldKeys;
+  cudaError_t e = cudaSuccess;
+  if (held) {
+    static std::atomic<uint64_t> done{0};
+    if ((e = allow_smem(evict_select_kernel<true>, kHeldKeys * 4, done)) != cudaSuccess) return e;
+  }
+  e = launch_after(held ? evict_select_kernel<true> : evict_select_kernel<false>, static_cast<unsigned>(rows), kThreads,
+                   held ? static_cast<int>(p.K.N) * 4 : 0, 1, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_after(p.K.D == 128 ? evict_gather_kernel<128> : evict_gather_kernel<64>, static_cast<unsigned>(ctas),
+                      256, 0, 1, s, p);
 }
 
 }  // namespace pbs

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassP
   constexpr int kTile = kGroup * D * 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wait_for_previous_kernel();
   const int M = static_cast<int>(p.Q.N), N = static_cast<int>(p.K.N), Hq = static_cast<int>(p.Q.H);
   const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
   const int part = static_cast<int>(blockIdx.x) % n_parts, bh = static_cast<int>(blockIdx.x) / n_parts;
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMas
   __shared__ int abort_sh;
   __shared__ __align__(16) float ny[kQStages][128];   // -log2(e) lse of the box's rows
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wait_for_previous_kernel();
   const int M = static_cast<int>(p.Q.N), N = static_cast<int>(p.K.N), Hq = static_cast<int>(p.Q.H);
   const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv, BH = static_cast<int>(p.K.B) * Hkv;
   const int part = static_cast<int>(blockIdx.x) % n_parts, rest = static_cast<int>(blockIdx.x) / n_parts;
@@ -385,8 +387,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMas
 
 __global__ void __launch_bounds__(256) mass_join_kernel(const KeyMassParams p, const int n_parts,
                                                         const double* __restrict__ partial) {
-  const int64_t N = p.K.N, BH = p.K.B * p.K.H, bh = blockIdx.y;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  wait_for_previous_kernel();
+  const int64_t N = p.K.N, BH = p.K.B * p.K.H, blocks = (N + 255) / 256, bh = blockIdx.x / blocks;
+  const int64_t j = blockIdx.x % blocks * 256 + threadIdx.x;
   if (j >= N) return;
   double sum = 0.0;
   for (int s = 0; s < n_parts; ++s) sum += partial[(s * BH + bh) * N + j];
@@ -414,29 +417,28 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
     // two CTAs per SM, and no more than there are rounds
     const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds, (8 * kSMs + BH - 1) / BH)));
     const int bytes = kWarps * kStages * kGroup * D * 2;
+    static std::atomic<uint64_t> done[2];
     auto kernel = rows <= 8 ? mass_few_kernel<D, 1> : mass_few_kernel<D, 2>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem(kernel, bytes, done[rows <= 8]);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(BH * parts), kWarps * 32, bytes, s>>>(p, parts);
-    return cudaGetLastError();
+    return launch_after(kernel, static_cast<unsigned>(BH * parts), kWarps * 32, bytes, 1, s, p, parts);
   }
   const int pm = static_cast<int>(std::min(p.Q.N, 128 / G));
   const int parts = mass_parts(p.Q, p.K);
   CUtensorMap mq, mk;
   if (!encode_queries_map(&mq, p.Q, static_cast<int>(G), pm, 1) || !encode_keys_map(&mk, p.K, 128))
     return cudaErrorNotSupported;
-  cudaError_t e = cudaFuncSetAttribute(mass_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       MassCfg<D>::kBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(mass_wide_kernel<D>, MassCfg<D>::kBytes, done);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (p.K.N + 127) / 128 * BH * parts;
   if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
   double* partial = static_cast<double*>(p.ws);
-  mass_wide_kernel<D><<<static_cast<unsigned>(ctas), kWideThreads, MassCfg<D>::kBytes, s>>>(p, parts, pm, partial, mq,
-                                                                                           mk);
-  if ((e = cudaGetLastError()) != cudaSuccess || parts == 1) return e;
-  mass_join_kernel<<<dim3(static_cast<unsigned>((p.K.N + 255) / 256), static_cast<unsigned>(BH)), 256, 0, s>>>(p, parts,
-                                                                                                           partial);
-  return cudaGetLastError();
+  e = launch_after(mass_wide_kernel<D>, static_cast<unsigned>(ctas), kWideThreads, MassCfg<D>::kBytes, 1, s, p, parts,
+                   pm, partial, mq, mk);
+  if (e != cudaSuccess || parts == 1) return e;
+  return launch_after(mass_join_kernel, static_cast<unsigned>((p.K.N + 255) / 256 * BH), 256, 0, 1, s, p, parts,
+                      partial);
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 // Warp-level fragments of the kernels that stream a cache for a few query rows:
-// cp.async groups, ldmatrix, and the bf16 mma m16n8k16.
+// cp.async groups, ldmatrix, the bf16 mma m16n8k16, and reads of a neighbour's
+// shared memory.
 #pragma once
 
 #include "pbs_common.cuh"
@@ -43,6 +44,21 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Distributed shared memory of the cluster, by mapa'd address.
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
+  float2 x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(a) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
 }
 
 }  // namespace pbs
