@@ -16,21 +16,25 @@
 // as 16-row boxes.  Tiles start at the first needed key, not at a multiple of
 // 128.
 //
-// Roles (384 threads): warp 0 issues tcgen05.mma and owns tensor memory; warp
-// 1 issues the TMA loads of Q and of the K and V rings; warps 2-3 clean the V
-// tiles that some row must not see in full (below); warps 4-7 and 8-11 run the
-// softmax of slot 0 and 1, one row per thread.  Tensor memory (512 columns):
-// S0 | S1 | O0 | O1; P (bf16) overwrites S and is the A operand of PV.  The
-// order of MMAs is fixed: PV of a slot's tile, then QK^T of its next tile, slots
-// in turn.
+// Roles (640 threads): warp 0 issues tcgen05.mma and owns tensor memory; warp
+// 1 issues the TMA loads of Q and of the K and V rings, the first ones before the
+// rest of the CTA is set up; warps 2-3 clean the V tiles that some row must not
+// see in full (below); warps 4-11 and 12-19 run the softmax of slot 0 and 1, two
+// threads per row with half of the tile's columns each, which agree on the row's
+// maximum through shared memory (one 64-thread barrier a tile).  One thread per
+// row left a scheduler with one softmax warp per slot, and that warp's chain of
+// maximum, exponentials and stores took 1.3 us a tile where the exponentials
+// alone take 0.5.  Tensor memory (512 columns): S0 | S1 | O0 | O1; P (bf16)
+// overwrites S and is the A operand of PV.  The order of MMAs is fixed: PV of a
+// slot's tile, then QK^T of its next tile, slots in turn.
 //
 // A masked key has weight 0, but 0 * NaN is NaN: where a tile holds a key that
 // some row of the CTA does not see, warps 2-3 replace NaN and infinities in V
 // by 0 before the product and note the key; at the end each row that does see
 // such a key takes those entries from global memory.
 //
-// Bound: the softmax.  A 128 x 128 tile costs 2 x 256 clocks of tensor core and
-// 1024 of the SM's 16 exponentials per clock; with few rows per CTA, HBM.
+// Bound: a 128 x 128 tile costs 2 x 540 clocks of tensor core and 1024 of the
+// SM's 16 exponentials per clock, so both; with few rows per CTA, HBM.
 #include <math.h>
 
 #include <algorithm>
@@ -43,7 +47,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // (select_sample.cu)
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr float kRescaleSlack = 8.0f;   // keep the running max while within 2^8
 // Tiles of a CTA that some row does not see in full: two per slot at the causal
 // end and two at the window's start (a slot spans at most 128 positions), one
@@ -80,25 +84,11 @@ __host__ __device__ __forceinline__ WideRows wide_rows(int64_t B, int64_t M, int
   return w;
 }
 
-// Rescale the first n16 x 16 P columns of this tile (bf16 pairs) by beta, after
-// this thread's earlier P stores have landed (rare; whole warps).
-__device__ __noinline__ void rescale_p(uint32_t tS, int n16, float beta) {
-  tmem_st_wait();
-  for (int q = 0; q < n16; ++q) {
-    uint32_t w[16];
-    tmem_ld16(tS + q * 16, w);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]));
-      w[e] = pack_bf16x2(f.x * beta, f.y * beta);
-    }
-    tmem_st16(tS + q * 16, w);
-  }
-}
+// Rescale a thread's half of its row of O by alpha (rare; whole warps).
 template <int D>
 __device__ __noinline__ void rescale_o(uint32_t tO, float alpha) {
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
+  for (int c = 0; c < D / 64; ++c) {
     uint32_t u[32];
     tmem_ld32(tO + c * 32, u);
 #pragma unroll
@@ -117,6 +107,7 @@ struct Shared {
   int any_bad;
   int dirty_tile[kMaxDirty];
   uint32_t bad[kMaxDirty][4];             // their keys with NaN or infinities in V
+  float row_max[2][2][2][128];            // [tile parity][slot][half][row]; then the sums
 };
 
 struct WideMaps {
@@ -171,23 +162,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   const int t0 = static_cast<int>(static_cast<int64_t>(T) * part / n_parts);
   const int t1 = static_cast<int>(static_cast<int64_t>(T) * (part + 1) / n_parts);
   // does slot h see any key of tile t, and do all its rows see all of them?
-  int hi_first[2], hi_last[2], lo_first[2], lo_last[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    hi_first[h] = hi_last[h] = prefix ? L - 1 : 0;
-    lo_first[h] = lo_last[h] = 0;
-    if (!prefix && h < n_slot) {
-      hi_first[h] = run.hi(first_pos(h));
-      hi_last[h] = run.hi(last_pos(h));
-      lo_first[h] = run.lo(first_pos(h), p.mask.window);
-      lo_last[h] = run.lo(last_pos(h), p.mask.window);
-    }
+  // (bounds of each slot's first and last rows, chosen without indexing so that
+  // they stay in registers)
+  int hi_first0 = L - 1, hi_last0 = L - 1, lo_first0 = 0, lo_last0 = 0;
+  int hi_first1 = L - 1, hi_last1 = L - 1, lo_first1 = 0, lo_last1 = 0;
+  if (!prefix) {
+    hi_first0 = run.hi(first_pos(0));
+    hi_last0 = run.hi(last_pos(0));
+    lo_first0 = run.lo(first_pos(0), p.mask.window);
+    lo_last0 = run.lo(last_pos(0), p.mask.window);
+    hi_first1 = run.hi(first_pos(1));
+    hi_last1 = run.hi(last_pos(1));
+    lo_first1 = run.lo(first_pos(1), p.mask.window);
+    lo_last1 = run.lo(last_pos(1), p.mask.window);
   }
   auto active = [&](int h, int t) {
-    return h < n_slot && 128 * t <= hi_last[h] && (128 * t + 127 >= lo_first[h] || 128 * t < run.n_sink);
+    const int up = h ? hi_last1 : hi_last0, low = h ? lo_first1 : lo_first0;
+    return h < n_slot && 128 * t <= up && (128 * t + 127 >= low || 128 * t < run.n_sink);
   };
   auto full = [&](int h, int t) {
-    return 128 * t + 127 <= hi_first[h] && (128 * t >= lo_last[h] || 128 * t + 127 < run.n_sink);
+    const int up = h ? hi_first1 : hi_first0, low = h ? lo_last1 : lo_last0;
+    return 128 * t + 127 <= up && (128 * t >= low || 128 * t + 127 < run.n_sink);
   };
   // (rows past the prefix are zeros, never NaN: no cleaning there)
   auto dirty = [&](int t) {
@@ -195,11 +190,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   };
 
   const uint32_t sQ = smem_u32(smem + C::kQ), sK = smem_u32(smem + C::kK), sV = smem_u32(smem + C::kV);
+  // ---- loads (warp 1, one thread): a K or V tile is one box per 64 columns, or
+  // 16-row boxes where it spans the end of the sinks
+  int raw[NS] = {};                                   // V tiles through bar_vraw, per stage
+  auto load_tile = [&](uint32_t dst, const CUtensorMap* one, const CUtensorMap* rows16, int head, int seq, int t,
+                       uint64_t* bar) {
+    mbar_expect_tx(bar, static_cast<uint32_t>(C::kTile));
+    const int v0 = 128 * t;
+    const bool mixed = run.delta > 0 && v0 < run.sink_end && v0 + 128 > run.sink_end;
+    for (int c = 0; c < D / 64; ++c) {
+      const uint32_t d = dst + c * (128 * 128);
+      if (!mixed) {
+        tma_rows_4d(d, one, c * 64, run.key(v0), head, seq, bar);
+      } else {
+        for (int r = 0; r < 128; r += 16) tma_rows_4d(d + r * 128, rows16, c * 64, run.key(v0 + r), head, seq, bar);
+      }
+    }
+  };
+  // (broadcast heads or sequences are one in the map)
+  auto load_k = [&](int t) {
+    const int st = (t - t0) % NS;
+    load_tile(sK + st * C::kTile, &maps.k, &maps.k16, (prefix ? p.Kp.sH : p.K.sH) == 0 ? 0 : hk,
+              p.K.sB == 0 ? 0 : b_own, t, &sh.bar_k[st]);
+  };
+  auto load_v = [&](int t) {
+    const int st = (t - t0) % NS;
+    const bool d = dirty(t);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) raw[q] += d && q == st;
+    load_tile(sV + st * C::kTile, &maps.v, &maps.v16, (prefix ? p.Vp.sH : p.V.sH) == 0 ? 0 : hk,
+              p.V.sB == 0 ? 0 : b_own, t, d ? &sh.bar_vraw[st] : &sh.bar_v[st]);
+  };
   if (tid == 32) {
     sh.abort = 0;
     sh.n_dirty = 0;
     sh.any_bad = 0;
-    for (int i = 0; i < kMaxDirty * 4; ++i) sh.bad[i / 4][i % 4] = 0u;
     mbar_init(&sh.bar_q, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sh.bar_k[i], 1);
@@ -210,16 +235,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sh.bar_s[h], 1);
-      mbar_init(&sh.bar_p[h], 4);
+      mbar_init(&sh.bar_p[h], 8);
       mbar_init(&sh.bar_o[h], 1);
     }
     mbar_init(&sh.bar_fin, 1);
     fence_mbar_init();
+    const int box = wr.pos_per_tile * wr.seqs_per_tile * G * 128;     // bytes of a 64-column Q box
+    mbar_expect_tx(&sh.bar_q, static_cast<uint32_t>(n_slot * (D / 64) * box));
+    for (int h = 0; h < n_slot; ++h)
+      for (int c = 0; c < D / 64; ++c)
+        tma_rows_4d(sQ + h * C::kTile + c * (128 * 128), &maps.q, c * 64, hk * G, tile_row(h), tile_seq(h), &sh.bar_q);
+    for (int t = t0; t < min(t0 + NS, t1); ++t) {
+      load_k(t);
+      load_v(t);
+    }
   }
   if (warp == 0) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
+  if (tid >= 64 && tid < 64 + kMaxDirty * 4) sh.bad[(tid - 64) / 4][(tid - 64) % 4] = 0u;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -229,41 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   if (warp == 1) {
     // ============================================================ producer
     if (lane == 0) {
-      const int box = wr.pos_per_tile * wr.seqs_per_tile * G * 128;     // bytes of a 64-column Q box
-      mbar_expect_tx(&sh.bar_q, static_cast<uint32_t>(n_slot * (D / 64) * box));
-      for (int h = 0; h < n_slot; ++h)
-        for (int c = 0; c < D / 64; ++c)
-          tma_rows_4d(sQ + h * C::kTile + c * (128 * 128), &maps.q, c * 64, hk * G, tile_row(h), tile_seq(h), &sh.bar_q);
-      // a K or V tile: one box per 64 columns, or 16-row boxes where it spans
-      // the end of the sinks (broadcast heads or sequences are one in the map)
-      const int kh = (prefix ? p.Kp.sH : p.K.sH) == 0 ? 0 : hk, vh = (prefix ? p.Vp.sH : p.V.sH) == 0 ? 0 : hk;
-      const int kbt = p.K.sB == 0 ? 0 : b_own, vbt = p.V.sB == 0 ? 0 : b_own;
-      auto tile = [&](uint32_t dst, const CUtensorMap* one, const CUtensorMap* rows16, int head, int seq, int t,
-                      uint64_t* bar) {
-        mbar_expect_tx(bar, static_cast<uint32_t>(C::kTile));
-        const int v0 = 128 * t;
-        const bool mixed = run.delta > 0 && v0 < run.sink_end && v0 + 128 > run.sink_end;
-        for (int c = 0; c < D / 64; ++c) {
-          const uint32_t d = dst + c * (128 * 128);
-          if (!mixed) {
-            tma_rows_4d(d, one, c * 64, run.key(v0), head, seq, bar);
-          } else {
-            for (int r = 0; r < 128; r += 16) tma_rows_4d(d + r * 128, rows16, c * 64, run.key(v0 + r), head, seq, bar);
-          }
-        }
-      };
-      int nk = t0, nv = t0, raw[NS] = {};             // tiles issued; of them through bar_vraw, per stage
-      for (int t = t0; t < t1; ++t) {
-        const int i = t - t0, st = i % NS;
-        const uint32_t again = ((i / NS) - 1) & 1;
-        if (i >= NS && !mbar_wait_or_abort(&sh.bar_kempty[st], again, p.err, abort_flag)) break;
-        tile(sK + st * C::kTile, &maps.k, &maps.k16, kh, kbt, t, &sh.bar_k[st]);
+      int nk = min(t0 + NS, t1), nv = nk;             // tiles issued
+      for (int t = t0 + NS; t < t1; ++t) {
+        const int st = (t - t0) % NS;
+        const uint32_t again = ((t - t0) / NS - 1) & 1;
+        if (!mbar_wait_or_abort(&sh.bar_kempty[st], again, p.err, abort_flag)) break;
+        load_k(t);
         ++nk;
-        if (i >= NS && !mbar_wait_or_abort(&sh.bar_vempty[st], again, p.err, abort_flag)) break;
-        const bool d = dirty(t);
-#pragma unroll
-        for (int q = 0; q < NS; ++q) raw[q] += d && q == st;
-        tile(sV + st * C::kTile, &maps.v, &maps.v16, vh, vbt, t, d ? &sh.bar_vraw[st] : &sh.bar_v[st]);
+        if (!mbar_wait_or_abort(&sh.bar_vempty[st], again, p.err, abort_flag)) break;
+        load_v(t);
         ++nv;
       }
       // no copy may be in flight when the CTA ends; without an abort the MMA
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
       for (; ok && seen <= t; ++seen) wait(&bars[(seen - t0) % NS], ((seen - t0) / NS) & 1);
     };
     auto last_user = [&](int h, int t) { return h == 1 || !active(1, t); };
-    int done[2] = {0, 0};                   // tiles whose QK^T has been issued, per slot
+    int done0 = 0, done1 = 0;               // tiles whose QK^T has been issued, per slot
     auto qk = [&](int h, int t) {
       landed(sh.bar_k, k_seen, t);
       if (!ok) return;
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
         if (last_user(h, t)) tc_commit(&sh.bar_kempty[st]);
       }
       __syncwarp();
-      ++done[h];
+      ++(h ? done1 : done0);
     };
     auto next = [&](int h, int t) {
       while (t < t1 && !active(h, t)) ++t;
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!ok || !active(h, t)) continue;
-        wait(&sh.bar_p[h], (done[h] - 1) & 1);
+        wait(&sh.bar_p[h], ((h ? done1 : done0) - 1) & 1);
         landed(sh.bar_v, v_seen, t);
         if (!ok) break;
         const int st = (t - t0) % NS;
@@ -367,22 +376,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
       for (int i = 0; i < NS; ++i)
         if (i == st) fill = seen[i]++;
       const bool got = mbar_wait_or_abort(&sh.bar_vraw[st], fill & 1, p.err, abort_flag);
-      if (named_sync_or(4, 64, !got)) break;
-      // thread x reads the same 16-byte chunks of rows x / 8, x / 8 + 8, ... of each half
+      if (named_sync_or(9, 64, !got)) break;
       uint4* v = reinterpret_cast<uint4*>(smem + C::kV + st * C::kTile);
-#pragma unroll 4
-      for (int i = x; i < C::kTile / 16; i += 64) {
-        uint4 w = v[i];
-        if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) | nonfinite_bf16x2(w.w)) {
-          w.x = finite_or_zero_bf16x2(w.x);
-          w.y = finite_or_zero_bf16x2(w.y);
-          w.z = finite_or_zero_bf16x2(w.z);
-          w.w = finite_or_zero_bf16x2(w.w);
-          v[i] = w;
-          const int row = i / 8 % 128;
-          if (128 * t + row < run.n) {
-            atomicOr(&sh.bad[n_dirty][row >> 5], 1u << (row & 31));
-            sh.any_bad = 1;
+      // adding 1 to an exponent of all ones carries into the sign bit
+      uint32_t bad = 0;
+#pragma unroll 1
+      for (int i = x; i < C::kTile / 16; i += 64 * 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = v[i + 64 * q];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          bad |= ((w[q].x & 0x7f807f80u) + 0x00800080u) | ((w[q].y & 0x7f807f80u) + 0x00800080u) |
+                 ((w[q].z & 0x7f807f80u) + 0x00800080u) | ((w[q].w & 0x7f807f80u) + 0x00800080u);
+      }
+      if (bad & 0x80008000u) {
+#pragma unroll 1
+        for (int i = x; i < C::kTile / 16; i += 64) {
+          uint4 w = v[i];
+          if (nonfinite_bf16x2(w.x) | nonfinite_bf16x2(w.y) | nonfinite_bf16x2(w.z) | nonfinite_bf16x2(w.w)) {
+            w.x = finite_or_zero_bf16x2(w.x);
+            w.y = finite_or_zero_bf16x2(w.y);
+            w.z = finite_or_zero_bf16x2(w.z);
+            w.w = finite_or_zero_bf16x2(w.w);
+            v[i] = w;
+            const int row = i / 8 % 128;
+            if (128 * t + row < run.n) {
+              atomicOr(&sh.bad[n_dirty][row >> 5], 1u << (row & 31));
+              sh.any_bad = 1;
+            }
           }
         }
       }
@@ -392,15 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
       }
       ++n_dirty;
       fence_proxy_async();
-      named_sync(4, 64);
+      named_sync(9, 64);
       if (x == 0) mbar_arrive(&sh.bar_v[st]);
     }
   } else {
     // ============================================================ softmax
-    const int h = (warp - 4) >> 2;
-    const int i = tid - 128 - h * 128;                // row of the tile = tensor-memory lane
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + h * 128 + lane_off, tO = tmem + 256 + h * 128 + lane_off;
+    const int h = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3;
+    const int i = quad * 32 + lane;                   // row of the tile = tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + h * 128 + lane_off, tO = tmem + 256 + h * 128 + half * (D / 2) + lane_off;
+    const uint32_t pair_bar = 1 + h * 4 + quad;       // the two warps of these 32 rows
     // the query row of this thread
     const int bb = tile_seq(h) + i / (wr.pos_per_tile * G), r = tile_row(h) + i / G % wr.pos_per_tile;
     bool valid = h < n_slot && i < wr.pos_per_tile * wr.seqs_per_tile * G && bb < B && r < M;
@@ -408,131 +431,152 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     const int pos = L - nq_own + r;
     const int hi = prefix ? L - 1 : run.hi(pos), lo = prefix ? 0 : run.lo(pos, p.mask.window);
     float m_run = -INFINITY, l_run = 0.f;
-    bool o_init = false, ok = true;
     int k = 0;
     for (int t = t0; t < t1; ++t) {
       if (!active(h, t)) continue;
-      if (!mbar_wait_or_abort(&sh.bar_s[h], k & 1, p.err, abort_flag)) ok = false;
+      // (after an abort the waits return at once; the loop still runs to its end,
+      // so that both warps take the same barriers)
+      mbar_wait_or_abort(&sh.bar_s[h], k & 1, p.err, abort_flag);
       tc_fence_after();
-      const bool masked = !full(h, t);
-      float psum = 0.f, m_t = m_run;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t x[64], u[32];
-        tmem_ld64(tS + c * 64, x);
-        if (masked) {
-          // indices v0 + e <= hi with v0 + e < n_sink or >= lo
-          const int v0 = 128 * t + c * 64, e_hi = hi - v0, e_lo = lo - v0, e_s = run.n_sink - v0;
+      uint32_t x[64];
+      tmem_ld64(tS + half * 64, x);
+      if (!full(h, t)) {
+        // columns e <= e_hi with e < e_s or e >= e_lo, as bits
+        const int v0 = 128 * t + half * 64, e_hi = hi - v0, e_lo = lo - v0, e_s = run.n_sink - v0;
+        auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };   // bits 0 .. n-1
+        const unsigned long long see = below(e_hi + 1) & (below(e_s) | ~below(e_lo));
+        const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e > e_hi || (e < e_lo && e >= e_s)) x[e] = __float_as_uint(-INFINITY);
-        }
-        float mm[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          mm[q] = fmax3(__uint_as_float(x[q]), __uint_as_float(x[8 + q]), __uint_as_float(x[16 + q]));
-          mm[q] = fmax3(mm[q], __uint_as_float(x[24 + q]), __uint_as_float(x[32 + q]));
-          mm[q] = fmax3(mm[q], __uint_as_float(x[40 + q]), __uint_as_float(x[48 + q]));
-          mm[q] = fmaxf(mm[q], __uint_as_float(x[56 + q]));
-        }
-        const float cm =
-            fmax3(fmax3(mm[0], mm[1], mm[2]), fmax3(mm[3], mm[4], mm[5]), fmaxf(mm[6], mm[7])) * p.scale_log2;
-        const bool up = cm > (m_t == -INFINITY ? -INFINITY : m_t + kRescaleSlack);
-        if (__any_sync(0xffffffffu, up)) {
-          const float m_new = up ? cm : m_t;
-          const float beta = m_new == -INFINITY ? 1.0f : ex2(m_t - m_new);
-          if (c > 0 && __any_sync(0xffffffffu, beta != 1.0f)) rescale_p(tS, 2 * c, beta);
-          psum *= beta;
-          m_t = m_new;
-        }
-        const float m_use = m_t == -INFINITY ? 0.f : m_t;
-        unsigned long long ps2[4] = {0ull, 0ull, 0ull, 0ull};
-        const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const unsigned long long y =
-              f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2);
-          float y0, y1;
-          f2_unpack(y, y0, y1);
-          const float a0 = ex2(y0), a1 = ex2(y1);
-          ps2[e & 3] = f2_add(ps2[e & 3], f2_pack(a0, a1));
-          u[e] = cvt_bf16x2(a0, a1);
-        }
-        float s0, s1, s2, s3, s4, s5, s6, s7;
-        f2_unpack(ps2[0], s0, s1);
-        f2_unpack(ps2[1], s2, s3);
-        f2_unpack(ps2[2], s4, s5);
-        f2_unpack(ps2[3], s6, s7);
-        psum += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
-        tmem_st32(tS + c * 32, u);
+        for (int e = 0; e < 64; ++e)
+          if (!((e < 32 ? see0 : see1) & (1u << (e & 31)))) x[e] = __float_as_uint(-INFINITY);
       }
-      const float alpha = m_t == -INFINITY ? 1.0f : ex2(m_run - m_t);
-      // (PV of this slot's previous tile has completed: the S-ready barrier
-      // tracks every MMA issued before this tile's QK^T)
-      if (o_init && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o<D>(tO, alpha);
-      l_run = l_run * alpha + psum;
-      m_run = m_t;
+      float mm[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        mm[q] = fmax3(__uint_as_float(x[q]), __uint_as_float(x[8 + q]), __uint_as_float(x[16 + q]));
+        mm[q] = fmax3(mm[q], __uint_as_float(x[24 + q]), __uint_as_float(x[32 + q]));
+        mm[q] = fmax3(mm[q], __uint_as_float(x[40 + q]), __uint_as_float(x[48 + q]));
+        mm[q] = fmaxf(mm[q], __uint_as_float(x[56 + q]));
+      }
+      float cm = fmax3(fmax3(mm[0], mm[1], mm[2]), fmax3(mm[3], mm[4], mm[5]), fmaxf(mm[6], mm[7])) * p.scale_log2;
+      // the other half's maximum; past this barrier both halves of S are read,
+      // so P may overwrite them
+      sh.row_max[k & 1][h][half][i] = cm;
+      named_sync(pair_bar, 64);
+      cm = fmaxf(cm, sh.row_max[k & 1][h][half ^ 1][i]);
+      // The running maximum moves only when the row's grows by more than 2^8, so
+      // P stays below 2^8 and O is rarely rescaled.  (PV of this slot's previous
+      // tile has completed: the S-ready barrier tracks every MMA before this QK^T.)
+      const bool up = cm > (m_run == -INFINITY ? -INFINITY : m_run + kRescaleSlack);
+      if (__any_sync(0xffffffffu, up)) {
+        const float m_new = up ? cm : m_run;
+        const float alpha = m_new == -INFINITY ? 1.0f : ex2(m_run - m_new);
+        if (k > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o<D>(tO, alpha);
+        l_run *= alpha;
+        m_run = m_new;
+      }
+      const float m_use = m_run == -INFINITY ? 0.f : m_run;
+      unsigned long long ps2[4] = {0ull, 0ull, 0ull, 0ull};
+      const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2), nm2 = f2_pack(-m_use, -m_use);
+      uint32_t u[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const unsigned long long y =
+            f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2);
+        float y0, y1;
+        f2_unpack(y, y0, y1);
+        const float a0 = ex2(y0), a1 = ex2(y1);
+        ps2[e & 3] = f2_add(ps2[e & 3], f2_pack(a0, a1));
+        u[e] = cvt_bf16x2(a0, a1);
+      }
+      tmem_st32(tS + half * 32, u);
+      float s0, s1, s2, s3, s4, s5, s6, s7;
+      f2_unpack(ps2[0], s0, s1);
+      f2_unpack(ps2[1], s2, s3);
+      f2_unpack(ps2[2], s4, s5);
+      f2_unpack(ps2[3], s6, s7);
+      l_run += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.bar_p[h]);
-      o_init = true;
       ++k;
     }
     // ---- epilogue
     if (h < n_slot) {
-      if (k > 0 && !mbar_wait_or_abort(&sh.bar_o[h], 0, p.err, abort_flag)) ok = false;
+      bool ok = k == 0 || mbar_wait_or_abort(&sh.bar_o[h], 0, p.err, abort_flag);
       tc_fence_after();
-      ok = !named_sync_or(2 + h, 128, !ok);
+      // the row's sum over both halves (the maxima of both parities may still be
+      // read: a barrier before and after)
+      named_sync(pair_bar, 64);
+      sh.row_max[0][h][half][i] = l_run;
+      named_sync(pair_bar, 64);
+      l_run += sh.row_max[0][h][half ^ 1][i];
+      if (!valid || k == 0) l_run = 0.f;
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       const int n_all = parts.prefix + parts.own, slot = prefix ? part : parts.prefix + part;
       const int64_t out = (static_cast<int64_t>(bb) * Hq + hk * G + i % G) * M + r;
       const int n_dirty = sh.any_bad ? sh.n_dirty : 0;
-      if (!valid || k == 0) l_run = 0.f;
-      const float inv = l_run == 0.f ? 0.f : 1.0f / l_run;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(const_cast<void*>(p.O.ptr)) + bb * p.O.sB +
-                         (hk * G + i % G) * p.O.sH + r * p.O.sN;
-      float* acc = parts.acc + (out * n_all + slot) * D;
+      const bool last = n_all == 1;                   // write the result, else this part's sums
+      const float inv = l_run == 0.f ? 0.f : last ? 1.0f / l_run : 1.0f;
+      unsigned char* dst =
+          last ? reinterpret_cast<unsigned char*>(static_cast<__nv_bfloat16*>(const_cast<void*>(p.O.ptr)) +
+                                                  bb * p.O.sB + (hk * G + i % G) * p.O.sH + r * p.O.sN + half * (D / 2))
+               : reinterpret_cast<unsigned char*>(parts.acc + (out * n_all + slot) * D + half * (D / 2));
+      // Rows go through shared memory (every MMA has completed, so the tiles are
+      // free), 32 columns of the warp's 32 rows at a time, so that a store covers
+      // whole runs of a row: 16-byte chunk c of row i lies at chunk c ^ (i mod 8).
+      uint4* stage = reinterpret_cast<uint4*>(smem + (warp - 4) * 4096);
+      const bool write = valid && (last || l_run != 0.f);
 #pragma unroll 1
-      for (int c = 0; ok && c < D / 32; ++c) {
+      for (int c = 0; ok && c < D / 64; ++c) {
         uint32_t u[32];
-        if (k > 0) {
-          tmem_ld32(tO + c * 32, u);
-        }
-        if (!valid) continue;
+        if (k > 0) tmem_ld32(tO + c * 32, u);
         if (l_run == 0.f) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) u[e] = 0u;
         }
         for (int q = 0; q < n_dirty * 128; ++q) {
-          if (!((sh.bad[q / 128][q / 32 % 4] >> (q % 32)) & 1u)) continue;
+          if (!valid || !((sh.bad[q / 128][q / 32 % 4] >> (q % 32)) & 1u)) continue;
           const int v = 128 * sh.dirty_tile[q / 128] + q % 128;
           if (v > hi || (v < lo && v >= run.n_sink)) continue;
           const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.V.ptr) + b_own * p.V.sB + hk * p.V.sH +
-                                    static_cast<int64_t>(run.key(v)) * p.V.sN + c * 32;
+                                    static_cast<int64_t>(run.key(v)) * p.V.sN + half * (D / 2) + c * 32;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const float f = __bfloat162float(vr[e]);
             if (!isfinite(f)) u[e] = __float_as_uint(__uint_as_float(u[e]) + f);
           }
         }
-        if (n_all == 1) {
+        const int chunks = last ? 4 : 8;              // of 16 bytes a row
+        if (last) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int e = 0; e < 4; ++e) {
             uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(u[e + 0]) * inv, __uint_as_float(u[e + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(u[e + 2]) * inv, __uint_as_float(u[e + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(u[e + 4]) * inv, __uint_as_float(u[e + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(u[e + 6]) * inv, __uint_as_float(u[e + 7]) * inv);
-            *reinterpret_cast<uint4*>(o + c * 32 + e) = w;
+            w.x = pack_bf16x2(__uint_as_float(u[8 * e + 0]) * inv, __uint_as_float(u[8 * e + 1]) * inv);
+            w.y = pack_bf16x2(__uint_as_float(u[8 * e + 2]) * inv, __uint_as_float(u[8 * e + 3]) * inv);
+            w.z = pack_bf16x2(__uint_as_float(u[8 * e + 4]) * inv, __uint_as_float(u[8 * e + 5]) * inv);
+            w.w = pack_bf16x2(__uint_as_float(u[8 * e + 6]) * inv, __uint_as_float(u[8 * e + 7]) * inv);
+            stage[lane * 8 + (e ^ (lane & 7))] = w;
           }
-        } else if (l_run != 0.f) {
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(acc + c * 32 + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            stage[lane * 8 + (e ^ (lane & 7))] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int q = lane; q < 32 * chunks; q += 32) {
+          const int row = q / chunks, e = q % chunks;
+          const uint4 w = stage[row * 8 + (e ^ (row & 7))];
+          unsigned char* to = reinterpret_cast<unsigned char*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+          if (__shfl_sync(0xffffffffu, write, row)) *reinterpret_cast<uint4*>(to + c * chunks * 16 + e * 16) = w;
+        }
+        __syncwarp();
       }
-      if (valid && ok) {
-        if (n_all > 1)
+      if (valid && ok && half == 0) {
+        if (!last)
           parts.ml[out * n_all + slot] = make_float2(l_run == 0.f ? -INFINITY : m_run, l_run);
         else if (p.lse)
           p.lse[out] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
