@@ -134,10 +134,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   const int n_parts = prefix ? parts.prefix : parts.own;
   const int pairs = (wr.tiles + 1) / 2;
   const int part = static_cast<int>(blockIdx.x) % n_parts;
-  const int rest = static_cast<int>(blockIdx.x) / n_parts;
-  const int pair = pairs - 1 - rest % pairs;          // without a window later positions have more keys: first
-  const int hk = rest / pairs % Hkv;
-  const int b_own = prefix ? 0 : rest / pairs / Hkv;
+  // (without a window later positions have more keys: first)
+  const int pair = pairs - 1 - static_cast<int>(blockIdx.x) / n_parts;
+  const int hk = static_cast<int>(blockIdx.y) % Hkv;
+  const int b_own = prefix ? 0 : static_cast<int>(blockIdx.y) / Hkv;
   const int nq_own = prefix ? M : cache_len(p.mask.q_len, b_own, M, p.err);
   const int L = prefix ? static_cast<int>(p.Kp.N) : cache_len(p.mask.kv_len, b_own, p.K.N, p.err);
   const int n_pos_tiles = (M + wr.pos_per_tile - 1) / wr.pos_per_tile;   // per sequence
@@ -240,15 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     }
     mbar_init(&sh.bar_fin, 1);
     fence_mbar_init();
-    const int box = wr.pos_per_tile * wr.seqs_per_tile * G * 128;     // bytes of a 64-column Q box
-    mbar_expect_tx(&sh.bar_q, static_cast<uint32_t>(n_slot * (D / 64) * box));
-    for (int h = 0; h < n_slot; ++h)
-      for (int c = 0; c < D / 64; ++c)
-        tma_rows_4d(sQ + h * C::kTile + c * (128 * 128), &maps.q, c * 64, hk * G, tile_row(h), tile_seq(h), &sh.bar_q);
-    for (int t = t0; t < min(t0 + NS, t1); ++t) {
-      load_k(t);
-      load_v(t);
-    }
   }
   if (warp == 0) {
     tmem_alloc(&sh.tmem_base, 512);
@@ -256,14 +247,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   }
   if (tid >= 64 && tid < 64 + kMaxDirty * 4) sh.bad[(tid - 64) / 4][(tid - 64) % 4] = 0u;
   tc_fence_before();
-  __syncthreads();
+  // warp 1 has nothing to wait for: it goes on to the first loads
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("bar.arrive 15, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    named_sync(15, kThreads);
+  }
   tc_fence_after();
-  const uint32_t tmem = sh.tmem_base;
+  const uint32_t tmem = sh.tmem_base;                 // (not warp 1's)
   volatile int* abort_flag = &sh.abort;
 
   if (warp == 1) {
     // ============================================================ producer
     if (lane == 0) {
+      const int box = wr.pos_per_tile * wr.seqs_per_tile * G * 128;     // bytes of a 64-column Q box
+      mbar_expect_tx(&sh.bar_q, static_cast<uint32_t>(n_slot * (D / 64) * box));
+      for (int h = 0; h < n_slot; ++h)
+        for (int c = 0; c < D / 64; ++c)
+          tma_rows_4d(sQ + h * C::kTile + c * (128 * 128), &maps.q, c * 64, hk * G, tile_row(h), tile_seq(h), &sh.bar_q);
+      for (int t = t0; t < min(t0 + NS, t1); ++t) {
+        load_k(t);
+        load_v(t);
+      }
       int nk = min(t0 + NS, t1), nv = nk;             // tiles issued
       for (int t = t0 + NS; t < t1; ++t) {
         const int st = (t - t0) % NS;
@@ -605,9 +611,9 @@ cudaError_t launch(const CacheAttnParams& p, const AttnParts& parts, bool prefix
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(attn_wide_kernel<D>, WideCfg<D>::kBytes, done);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = wide_units(p.Q, p.K, prefix) * (prefix ? parts.prefix : parts.own);
-  return launch_after(attn_wide_kernel<D>, static_cast<unsigned>(ctas), kThreads, WideCfg<D>::kBytes, 1, s, p, parts,
-                      prefix, wr, maps);
+  const dim3 grid(static_cast<unsigned>((wr.tiles + 1) / 2 * (prefix ? parts.prefix : parts.own)),
+                  static_cast<unsigned>(p.K.H * (prefix ? 1 : p.K.B)));
+  return launch_after(attn_wide_kernel<D>, grid, kThreads, WideCfg<D>::kBytes, 1, s, p, parts, prefix, wr, maps);
 }
 
 }  // namespace

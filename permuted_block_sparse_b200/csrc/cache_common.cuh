@@ -17,7 +17,7 @@ constexpr int kSMs = 148;   // B200
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, int threads, int smem, int cluster, cudaStream_t s,
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s,
                          Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2] = {};
@@ -26,7 +26,7 @@ cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, int threads, 
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
