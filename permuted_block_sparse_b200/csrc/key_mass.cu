@@ -34,12 +34,15 @@ __device__ __forceinline__ void write_mass(const KeyMassParams& p, int64_t bh, i
 // as the B operand.  A CTA's rounds of 64 keys are spread over the cache, so
 // that the keys outside a window, which are not loaded, fall on all CTAs alike.
 // Bound: HBM, 2 D bytes per visible key.
+// Sixteen warps per SM (four CTAs of 48 KB) hide the chain from a group's arrival
+// to its sums; with eight the schedulers issued in 41% of the cycles.
 constexpr int kWarps = 4;
-constexpr int kStages = 6;
+constexpr int kStages = 3;
 constexpr int kGroup = 16;
+constexpr int kFewCtas = 4;                       // per SM
 
 template <int D, int NG>
-__global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassParams p, const int n_parts) {
+__global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const KeyMassParams p, const int n_parts) {
   constexpr int kTile = kGroup * D * 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -49,12 +52,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassP
   const int part = static_cast<int>(blockIdx.x) % n_parts, bh = static_cast<int>(blockIdx.x) / n_parts;
   const int b = bh / Hkv, hk = bh % Hkv;
   const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
-  const int64_t window = p.mask.window;
-  const int n_sink = p.mask.n_sink;
+  const int window = static_cast<int>(p.mask.window), n_sink = p.mask.n_sink;
   const int first = L - nq;                       // position of row 0
   // keys that some row sees: j < n_sink or j >= lo_min (and j < L); keys that every row sees end at `first`
-  const int lo_min = static_cast<int>(max(static_cast<int64_t>(0), first - window + 1));
-  const int lo_max = static_cast<int>(max(static_cast<int64_t>(0), L - window));
+  const int lo_min = max(0, first - window + 1);
+  const int lo_max = max(0, L - window);
   const int seen_end = nq > 0 ? L : 0;
 
   uint32_t qb[NG][D / 16][2];                     // Q as B fragments: row lane / 4 of each eight
@@ -85,33 +87,49 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassP
       }
     }
   }
-  const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + hk * p.K.sH;
   const uint32_t ring = smem_u32(smem + warp * kStages * kTile);
   constexpr int CH = D / 8, RPI = 32 / CH;
   const int lc = lane % CH, lr = lane / CH;
-  auto base = [&](int i) { return ((static_cast<int64_t>(i) * n_parts + part) * kWarps + warp) * kGroup; };
-  auto some = [&](int64_t j0) { return j0 < seen_end && (j0 + kGroup > lo_min || j0 < n_sink); };
-  auto load = [&](int i, int st) {
-    const int64_t j0 = base(i);
+  // this lane's chunk of its rows of group 0, and from there to its next row
+  const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + hk * p.K.sH + lc * 8;
+  const int64_t sN = p.K.sN;
+  const int stride = n_parts * kWarps * kGroup;
+  auto some = [&](int j0) { return j0 < seen_end && (j0 + kGroup > lo_min || j0 < n_sink); };
+  auto load = [&](int j0, int st) {
     if (some(j0)) {
+      const uint32_t dst = ring + st * kTile;
+      if (j0 + kGroup <= L && (j0 >= lo_min || j0 + kGroup <= n_sink)) {
+        const __nv_bfloat16* src = kb + (j0 + lr) * sN;
 #pragma unroll
-      for (int it = 0; it < kGroup / RPI; ++it) {
-        const int r = it * RPI + lr;
-        const int64_t j = j0 + r;
-        const bool ok = j < L && (j >= lo_min || j < n_sink);
-        cp_async16_zfill(ring + st * kTile + rows_offset<D>(r, lc), kb + (ok ? j : 0) * p.K.sN + lc * 8, ok);
+        for (int it = 0; it < kGroup / RPI; ++it, src += RPI * sN) cp_async16(dst + rows_offset<D>(it * RPI + lr, lc), src);
+      } else {
+#pragma unroll
+        for (int it = 0; it < kGroup / RPI; ++it) {
+          const int j = j0 + it * RPI + lr;
+          const bool ok = j < L && (j >= lo_min || j < n_sink);
+          cp_async16_zfill(dst + rows_offset<D>(it * RPI + lr, lc), kb + (ok ? j : 0) * sN, ok);
+        }
       }
     }
     cp_async_commit();
   };
+  // the lanes (lane mod 4) < 2 write keys 8 (lane mod 4) + lane / 4; their earlier
+  // mass is read a round ahead, or its latency would be paid every round
+  const int mine = (lane & 3) * 8 + lane / 4;
+  const float* prev = p.prev && (lane & 3) < 2 ? p.prev + bh * p.prev_stride + mine : nullptr;
+  float* mass = p.mass + bh * p.mass_stride + mine;
+  auto earlier = [&](int j0) { return prev && j0 + mine < L ? prev[j0] : 0.f; };
+  int j0 = (part * kWarps + warp) * kGroup;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load(i, i);
+  for (int i = 0; i < kStages - 1; ++i) load(j0 + i * stride, i);
   int st = 0;
-  for (int i = 0; base(i) < N; ++i) {
+  float next_old = earlier(j0);
+  for (; j0 < N; j0 += stride) {
+    const float old = next_old;
+    next_old = earlier(j0 + stride);
     cp_async_wait<kStages - 2>();
     __syncwarp();
-    load(i + kStages - 1, st == 0 ? kStages - 1 : st - 1);
-    const int64_t j0 = base(i);
+    load(j0 + (kStages - 1) * stride, st == 0 ? kStages - 1 : st - 1);
     const uint32_t sk = ring + st * kTile;
     st = st == kStages - 1 ? 0 : st + 1;
     float sum[2] = {0.f, 0.f};                    // keys lane / 4 and 8 + lane / 4
@@ -129,15 +147,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassP
 #pragma unroll
         for (int g = 0; g < NG; ++g) mma_16816(s[g], f[0], f[1], f[2], f[3], qb[g][k][0], qb[g][k][1]);
       }
-      const bool full = j0 + kGroup - 1 <= first && j0 + kGroup <= L && (j0 >= lo_max || j0 + kGroup <= n_sink);
+      const bool full = j0 + kGroup - 1 <= first && (j0 >= lo_max || j0 + kGroup <= n_sink);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float w = ex2(fmaf(s[g][e], p.scale_log2, -y[g][e & 1]));
           if (!full) {
-            const int64_t j = j0 + (e >> 1) * 8 + lane / 4;
-            const int at = pos[g][e & 1];
+            const int j = j0 + (e >> 1) * 8 + lane / 4, at = pos[g][e & 1];
             if (j > at || (j <= at - window && j >= n_sink)) w = 0.f;
           }
           sum[e >> 1] += w;
@@ -149,10 +166,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) mass_few_kernel(const KeyMassP
         sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
       }
     }
-    if ((lane & 3) < 2) {
-      const int64_t j = j0 + (lane & 3) * 8 + lane / 4;
-      if (j < N) write_mass(p, bh, j, L, (lane & 3) ? sum[1] : sum[0]);
-    }
+    if ((lane & 3) < 2 && j0 + mine < N)
+      mass[j0] = j0 + mine < L ? fmaf(p.decay, old, (lane & 3) ? sum[1] : sum[0]) : 0.f;
   }
   cp_async_wait_all();
 }
@@ -414,8 +429,10 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
   const int64_t G = p.Q.H / p.K.H, rows = p.Q.N * G, BH = p.K.B * p.K.H;
   if (rows <= kFewRows) {
     const int64_t rounds = (p.K.N + kWarps * kGroup - 1) / (kWarps * kGroup);
-    // two CTAs per SM, and no more than there are rounds
-    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds, (8 * kSMs + BH - 1) / BH)));
+    // One CTA for every place on the chip, with two rounds of keys at least: 8
+    // KV-head rows of 4096 keys take 4.0 us in 32 parts (6.0 in 8), 32 rows of
+    // 8192 11.3 us in 16 (21.5 in 128).
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds / 2, (kFewCtas * kSMs + BH - 1) / BH)));
     const int bytes = kWarps * kStages * kGroup * D * 2;
     static std::atomic<uint64_t> done[2];
     auto kernel = rows <= 8 ? mass_few_kernel<D, 1> : mass_few_kernel<D, 2>;
