@@ -173,86 +173,96 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
 }
 
 // ------------------------------------------------------------------ many rows
-// One CTA per (128 keys, KV head, sequence, part of the query rows), the heaviest
-// key tiles (the first, which the most rows see) first.  The key tile stays in
-// shared memory as the A operand; the query rows stream past in TMA boxes packed
-// as (position, head of the group), up to 128 a box, as the B operand.
-//   warp 0  issues S^T = K Q^T into two tensor-memory buffers;
-//   warp 1  loads K once and the query boxes with their lse into a two-stage ring;
-//   warps 2-5 (one key per thread) take 2^(x - y) of every column and sum it.
-// Two CTAs per SM (96 KB and 256 tensor-memory columns each), so that one's
-// set-up hides behind the other.  Bound: exponentials, 16 per clock and SM.
-constexpr int kWideThreads = 192;
-constexpr int kQStages = 2;
+// One CTA per (256 keys, KV head, sequence, part of the query rows), the heaviest
+// key tiles (the first, which the most rows see) first.  Two tiles of 128 keys stay
+// in tensor memory as A operands; the query rows stream past in TMA boxes packed as
+// (position, head of the group), up to 128 a box, as the B operand of both.  (With
+// A in shared memory too, a 128 x 128 product reads both operands from there and
+// took 0.65 us of an SM, and with one tile a box its boxes 7 TB/s of L2.)
+//   warp 0  issues S^T = K Q^T, box by box for both tiles, into a ring of three
+//     tensor-memory buffers;
+//   warp 1  loads K once and the query boxes and their lse into rings of four;
+//   warps 2-17 copy K into tensor memory, then take 2^(x - y) of every column and
+//     sum it: a thread has one key and 64 of the 128 columns.
+// Bound: exponentials, 16 per clock and SM on the SFU.
+constexpr int kWideThreads = 576;
+constexpr int kConsumerWarps = 16;
+constexpr int kQStages = 4;
 
 template <int D>
 struct MassCfg {
   static constexpr int kTile = (D / 64) * 128 * 128;
-  static constexpr int kBytes = (1 + kQStages) * kTile + 1024;
+  static constexpr int kBytes = (2 + kQStages) * kTile + 1024;
+  static constexpr int kSmem = kBytes > 120 * 1024 ? kBytes : 120 * 1024;   // one CTA per SM: all of tensor memory
 };
 
 template <int D>
-__global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMassParams p, const int n_parts,
+__global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMassParams p, const int n_parts,
                                                                     const int pm, double* __restrict__ partial,
                                                                     const __grid_constant__ CUtensorMap mq,
                                                                     const __grid_constant__ CUtensorMap mk) {
   using C = MassCfg<D>;
+  constexpr int NS = kQStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bar_k, bar_q[kQStages], bar_qempty[kQStages], bar_s[2], bar_sfree[2];
+  __shared__ uint64_t bar_k, bar_q[NS], bar_qempty[NS], bar_y[NS], bar_yempty[NS], bar_a, bar_s[3], bar_sfree[3];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_sh;
-  __shared__ __align__(16) float ny[kQStages][128];   // -log2(e) lse of the box's rows
+  __shared__ __align__(16) float ny[NS][128];         // -log2(e) lse of the box's rows
+  __shared__ double half_sum[256];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_previous_kernel();
   const int M = static_cast<int>(p.Q.N), N = static_cast<int>(p.K.N), Hq = static_cast<int>(p.Q.H);
   const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv, BH = static_cast<int>(p.K.B) * Hkv;
   const int part = static_cast<int>(blockIdx.x) % n_parts, rest = static_cast<int>(blockIdx.x) / n_parts;
-  const int bh = rest % BH, j0 = rest / BH * 128, b = bh / Hkv, hk = bh % Hkv;
+  const int bh = rest % BH, j0 = rest / BH * 256, b = bh / Hkv, hk = bh % Hkv;
   const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
   const int64_t window = p.mask.window, first = L - nq;
   const int n_sink = p.mask.n_sink;
-  // query rows that see some key of this tile: r0 <= r < r1, then this part's boxes of pm positions
-  const int64_t last_key = min(j0 + 127, L - 1);
+  // query rows that see some key of these tiles: r0 <= r < r1, then this part's boxes of pm positions
+  const int64_t last_key = min(j0 + 255, L - 1);
   int64_t r0 = max(static_cast<int64_t>(0), j0 - first), r1 = nq;
   if (j0 >= n_sink) r1 = min(r1, last_key + window - first);
   if (j0 >= L || r1 <= r0) r0 = r1 = 0;
   const int n_box = static_cast<int>((r1 - r0 + pm - 1) / pm);
   const int x0 = static_cast<int>(static_cast<int64_t>(n_box) * part / n_parts);
   const int x1 = static_cast<int>(static_cast<int64_t>(n_box) * (part + 1) / n_parts);
-  const int cols = pm * G, n_mma = (cols + 15) / 16 * 16;
+  const int cols = pm * G, n_mma = (cols + 15) / 16 * 16, n_tile = j0 + 128 < L ? 2 : 1;
   double* mine = n_parts > 1 ? partial + (static_cast<int64_t>(part) * BH + bh) * N : nullptr;
   if (x0 == x1) {                                 // nothing sees these keys here
-    if (tid < 128 && j0 + tid < N) {
+    if (tid < 256 && j0 + tid < N) {
       if (mine) mine[j0 + tid] = 0.0;
       else write_mass(p, bh, j0 + tid, L, 0.0);
     }
     return;
   }
 
-  const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + C::kTile);
+  const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + 2 * C::kTile);
   // MMA columns past the box: zero rows (the boxes never write them)
-  for (int i = tid; i < kQStages * (n_mma - cols) * (D / 8); i += kWideThreads) {
+  for (int i = tid; i < NS * (n_mma - cols) * (D / 8); i += kWideThreads) {
     const int c = i % (D / 8), r = cols + i / (D / 8) % (n_mma - cols), s = i / (D / 8) / (n_mma - cols);
-    *reinterpret_cast<uint4*>(smem + (1 + s) * C::kTile + (c / 8) * (128 * 128) + sw128_offset(r, c % 8)) =
+    *reinterpret_cast<uint4*>(smem + (2 + s) * C::kTile + (c / 8) * (128 * 128) + sw128_offset(r, c % 8)) =
         make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async();
   if (warp == 0) {
-    tmem_alloc(&tmem_base, 256);
+    tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
   if (tid == 32) {
     abort_sh = 0;
     mbar_init(&bar_k, 1);
-    for (int i = 0; i < kQStages; ++i) {
-      mbar_init(&bar_q[i], 33);                   // the box's bytes, and each lane's lse
-      mbar_init(&bar_qempty[i], 5);               // the MMAs, and the consumer warps' use of the lse
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bar_q[i], 1);
+      mbar_init(&bar_qempty[i], 1);
+      mbar_init(&bar_y[i], 32);
+      mbar_init(&bar_yempty[i], 8 * n_tile);
     }
-    for (int i = 0; i < 2; ++i) {
+    mbar_init(&bar_a, 8 * n_tile);
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_sfree[i], 4);
+      mbar_init(&bar_sfree[i], 8);
     }
     fence_mbar_init();
   }
@@ -265,111 +275,173 @@ __global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMas
   if (warp == 1) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      mbar_expect_tx(&bar_k, C::kTile);
-      for (int c = 0; c < D / 64; ++c)
-        tma_rows_4d(sK + c * (128 * 128), &mk, c * 64, j0, p.K.sH == 0 ? 0 : hk, p.K.sB == 0 ? 0 : b, &bar_k);
+      mbar_expect_tx(&bar_k, static_cast<uint32_t>(n_tile * C::kTile));
+      for (int h = 0; h < n_tile; ++h)
+        for (int c = 0; c < D / 64; ++c)
+          tma_rows_4d(sK + h * C::kTile + c * (128 * 128), &mk, c * 64, j0 + 128 * h, p.K.sH == 0 ? 0 : hk,
+                      p.K.sB == 0 ? 0 : b, &bar_k);
     }
-    auto lse_of = [&](int x, float (&v)[4]) {     // this lane's rows lane, lane + 32, ... of box x
+    auto load_box = [&](int x) {                  // (one lane)
+      const int s = (x - x0) % NS;
+      mbar_expect_tx(&bar_q[s], static_cast<uint32_t>(cols * D * 2));
+      for (int c = 0; c < D / 64; ++c)
+        tma_rows_4d(sQ + s * C::kTile + c * (128 * 128), &mq, c * 64, hk * G, static_cast<int>(r0 + x * pm), b,
+                    &bar_q[s]);
+    };
+    int issued = min(x1, x0 + NS);
+    if (lane == 0)
+      for (int x = x0; x < issued; ++x) load_box(x);
+    // The lse of this lane's rows lane, lane + 32, ... of box x, of four boxes at a
+    // time and four boxes ahead: one at a time, one ahead, its latency was what
+    // every box took.
+    const float* lse[4];
+    int in_box[4];                                // the row's position in the box; past its end: never a query
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = lane + 32 * e;
+      in_box[e] = c < cols ? c / G : 0x40000000;
+      lse[e] = p.lse + (static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + r0 + c / G;
+    }
+    const int n_left = static_cast<int>(nq - r0);
+    auto lse_of = [&](int x, float (&v)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int c = lane + 32 * e;
-        const int64_t r = r0 + static_cast<int64_t>(x) * pm + c / G;
-        const float l = c < cols && r < nq ? p.lse[(static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + r] : -INFINITY;
+        const float l = x < x1 && x * pm + in_box[e] < n_left ? lse[e][x * pm] : -INFINITY;
         v[e] = l == -INFINITY ? -INFINITY : -l * kLog2e;    // -inf: the row adds nothing
       }
     };
-    float v[4];
-    lse_of(x0, v);
-    int issued = x0;
+    float v[NS][4], ahead[NS][4];
     bool ok = true;
-    for (int x = x0; ok && x < x1; ++x) {
-      const int i = x - x0, s = i % kQStages;
-      if (i >= kQStages)
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_or_abort(&bar_qempty[s], ((i / kQStages) - 1) & 1, p.err, abort_flag));
-      if (!ok) break;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ny[s][lane + 32 * e] = v[e];
-      if (lane == 0) {
-        mbar_expect_tx(&bar_q[s], static_cast<uint32_t>(cols * D * 2));
-        for (int c = 0; c < D / 64; ++c)
-          tma_rows_4d(sQ + s * C::kTile + c * (128 * 128), &mq, c * 64, hk * G, static_cast<int>(r0 + x * pm), b,
-                      &bar_q[s]);
+    for (int q = 0; q < NS; ++q) lse_of(x0 + q, v[q]);
+    for (int xb = x0; ok && xb < x1; xb += NS) {
+#pragma unroll
+      for (int q = 0; q < NS; ++q) lse_of(xb + NS + q, ahead[q]);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int x = xb + s, i = x - x0;
+        if (x >= x1 || !ok) break;
+        if (i >= NS) {
+          ok = mbar_wait_or_abort(&bar_qempty[s], (i / NS - 1) & 1, p.err, abort_flag);
+          if (ok = __all_sync(0xffffffffu, ok); !ok) break;
+          if (lane == 0) load_box(x);
+          issued = x + 1;
+          ok = mbar_wait_or_abort(&bar_yempty[s], (i / NS - 1) & 1, p.err, abort_flag);
+          if (ok = __all_sync(0xffffffffu, ok); !ok) break;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ny[s][lane + 32 * e] = v[s][e];
+        mbar_arrive(&bar_y[s]);
       }
-      mbar_arrive(&bar_q[s]);
-      issued = x + 1;
-      if (x + 1 < x1) lse_of(x + 1, v);
+#pragma unroll
+      for (int q = 0; q < NS; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[q][e] = ahead[q][e];
     }
     // no copy may be in flight when the CTA ends; without an abort the other
     // roles have waited for all of them
     if (*abort_flag) {
       mbar_wait(&bar_k, 0, p.err);
-      for (int x = max(x0, issued - kQStages); x < issued; ++x)
-        mbar_wait(&bar_q[(x - x0) % kQStages], ((x - x0) / kQStages) & 1, p.err);
+      for (int x = max(x0, issued - NS); x < issued; ++x)
+        mbar_wait(&bar_q[(x - x0) % NS], ((x - x0) / NS) & 1, p.err);
     }
   } else if (warp == 0) {
     // ---------------------------------------------------------------- MMA
     const uint32_t idesc = idesc_bf16(128, n_mma, false);
-    bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bar_k, 0, p.err, abort_flag));
+    bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bar_a, 0, p.err, abort_flag));
+    int u = 0, d = 0, par = 0;                    // products so far; the next one's buffer and its parity
     for (int x = x0; ok && x < x1; ++x) {
-      const int i = x - x0, s = i % kQStages, d = i & 1;
-      ok = mbar_wait_or_abort(&bar_q[s], (i / kQStages) & 1, p.err, abort_flag);
-      if (ok && i >= 2) ok = mbar_wait_or_abort(&bar_sfree[d], ((i / 2) - 1) & 1, p.err, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t a0 = sdesc_sw128(sK, 16, 1024), b0 = sdesc_sw128(sQ + s * C::kTile, 16, 1024);
+      const int i = x - x0, s = i % NS;
+      ok = mbar_wait_or_abort(&bar_q[s], (i / NS) & 1, p.err, abort_flag);
+      const uint64_t b0 = sdesc_sw128(sQ + s * C::kTile, 16, 1024);
+      for (int h = 0; h < n_tile; ++h, ++u) {
+        if (ok && u >= 3) ok = mbar_wait_or_abort(&bar_sfree[d], par ^ 1, p.err, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * (128 * 128) + (kk % 4) * 32;
-        if (elect_one()) mma_ss(tmem + d * 128, sdesc_add(a0, off), sdesc_add(b0, off), idesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * (128 * 128) + (kk % 4) * 32;
+          if (elect_one())
+            mma_ts(tmem + 128 + d * 128, tmem + h * 64 + kk * 8, sdesc_add(b0, off), idesc, kk > 0 ? 1u : 0u);
+        }
+        if (elect_one()) {
+          tc_commit(&bar_s[d]);
+          if (h == n_tile - 1) tc_commit(&bar_qempty[s]);
+        }
+        __syncwarp();
+        if (++d == 3) {
+          d = 0;
+          par ^= 1;
+        }
       }
-      if (elect_one()) {
-        tc_commit(&bar_s[d]);
-        tc_commit(&bar_qempty[s]);
-      }
-      __syncwarp();
     }
   } else {
     // ----------------------------------------------------------- consumers
-    const int key = (warp & 3) * 32 + lane;       // tensor-memory lane
+    const int tile = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1;
+    const int key = tile * 128 + (warp & 3) * 32 + lane;      // lane of tensor memory within the tile
     const int64_t j = j0 + key;
-    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + 128 + half * 64 + lanes;
     const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2);
     double sum = 0.0;
-    for (int x = x0; x < x1; ++x) {
-      const int i = x - x0, s = i % kQStages, d = i & 1;
+    if (tile < n_tile) {
+      // this key's half of its row into tensor memory: column c holds elements 2c, 2c + 1
+      mbar_wait_or_abort(&bar_k, 0, p.err, abort_flag);
+      const unsigned char* row = smem + tile * C::kTile;
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {          // 32 elements at a time
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int chunk = half * (D / 16) + q * 4 + e;
+          const uint4 v = *reinterpret_cast<const uint4*>(row + (chunk / 8) * (128 * 128) +
+                                                          sw128_offset(key & 127, chunk % 8));
+          w[4 * e] = v.x;
+          w[4 * e + 1] = v.y;
+          w[4 * e + 2] = v.z;
+          w[4 * e + 3] = v.w;
+        }
+        tmem_st16(tmem + tile * 64 + half * (D / 4) + q * 16 + lanes, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_a);
+    }
+    for (int x = x0; tile < n_tile && x < x1; ++x) {
+      const int i = x - x0, s = i % NS, u = i * n_tile + tile, d = u % 3;
       // (after an abort the waits return at once; the sums are then meaningless
       // and the error word says so)
-      mbar_wait_or_abort(&bar_q[s], (i / kQStages) & 1, p.err, abort_flag);
-      mbar_wait_or_abort(&bar_s[d], (i / 2) & 1, p.err, abort_flag);
+      mbar_wait_or_abort(&bar_y[s], (i / NS) & 1, p.err, abort_flag);
+      mbar_wait_or_abort(&bar_s[d], (u / 3) & 1, p.err, abort_flag);
       tc_fence_after();
       // rows of the box that see this key: c_lo <= c < c_hi
       const int64_t row = r0 + static_cast<int64_t>(x) * pm, at = first + row;
       const int64_t hi = j < n_sink ? nq - row : min(nq - row, j + window - at);
       const int c_lo = static_cast<int>(min(static_cast<int64_t>(pm), max(static_cast<int64_t>(0), j - at))) * G;
       const int c_hi = j < L ? static_cast<int>(min(static_cast<int64_t>(pm), max(static_cast<int64_t>(0), hi))) * G : 0;
-      const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == cols);
+      const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128);
+      const bool none = __all_sync(0xffffffffu, c_lo >= c_hi);
       unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
-      for (int c = 0; c < n_mma; c += 32) {
-        uint32_t u[32];
-        tmem_ld32(tS + d * 128 + c, u);
-        if (!full) {
+      for (int c = half * 64; c < min(none ? 0 : n_mma, half * 64 + 64); c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tS + d * 128 + (c & 32), v);
+        if (!full) {                              // (columns past the box are past c_hi)
           const int lo = c_lo - c, up = c_hi - c;
+          const uint32_t see = (up <= 0 ? 0u : up >= 32 ? ~0u : (1u << up) - 1u) &
+                               ~(lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1u);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (e < lo || e >= up) u[e] = __float_as_uint(-INFINITY);
-        } else if (c + 32 > n_mma) {              // (the last 16 columns of the buffer hold nothing)
-#pragma unroll
-          for (int e = 16; e < 32; ++e) u[e] = __float_as_uint(-INFINITY);
+            if (!(see & (1u << e))) v[e] = __float_as_uint(-INFINITY);
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(&ny[s][c + e]);
           float t0, t1, t2, t3;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), sc2, n2.x), t0, t1);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])), sc2, n2.y), t2, t3);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, n2.x), t0, t1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, n2.y), t2, t3);
           a2[(e / 2) & 3] = f2_add(a2[(e / 2) & 3], f2_pack(ex2(t0), ex2(t1)));
           a2[(e / 2 + 1) & 3] = f2_add(a2[(e / 2 + 1) & 3], f2_pack(ex2(t2), ex2(t3)));
         }
@@ -378,7 +450,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMas
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bar_sfree[d]);
-        mbar_arrive(&bar_qempty[s]);
+        mbar_arrive(&bar_yempty[s]);
       }
       float s0, s1, s2, s3, s4, s5, s6, s7;
       f2_unpack(a2[0], s0, s1);
@@ -387,7 +459,10 @@ __global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMas
       f2_unpack(a2[3], s6, s7);
       sum += static_cast<double>(((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7)));
     }
-    if (j < N) {
+    if (half == 1) half_sum[key] = sum;
+    named_sync(1, kConsumerWarps * 32);
+    if (half == 0 && j < N) {
+      sum += half_sum[key];
       if (mine) mine[j] = sum;
       else write_mass(p, bh, j, L, sum);
     }
@@ -396,7 +471,233 @@ __global__ void __launch_bounds__(kWideThreads, 2) mass_wide_kernel(const KeyMas
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------- some hundred rows
+// Up to 256 query rows per KV head (drafted tokens, the last rows of a prompt).  The
+// other way round: the queries (one or two boxes) and their lse stay in shared memory
+// and the key tiles stream past, through a ring of four, in pairs that two groups of
+// eight consumer warps take.  Each group has two tensor-memory buffers.  CTAs are
+// one per SM; those of one (sequence, KV head) share its visible tiles in turn.
+// Bound: HBM for the keys, with many rows the exponentials.
+constexpr int kKStages = 4;
+
+template <int D>
+struct MidCfg {
+  static constexpr int kTile = (D / 64) * 128 * 128;
+  static constexpr int kBytes = (2 + kKStages) * kTile + 1024;
+  static constexpr int kSmem = kBytes > 120 * 1024 ? kBytes : 120 * 1024;   // one CTA per SM: all of tensor memory
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMassParams p, const int n_parts,
+                                                                   const int pm,
+                                                                   const __grid_constant__ CUtensorMap mq,
+                                                                   const __grid_constant__ CUtensorMap mk) {
+  using C = MidCfg<D>;
+  constexpr int NS = kKStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bar_q, bar_k[NS], bar_kempty[NS], bar_s[4], bar_sfree[4];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_sh;
+  __shared__ __align__(16) float ny[2][128];          // -log2(e) lse of the boxes' rows
+  __shared__ float group_sum[2][2][128];              // [group][parity of the pair][key]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wait_for_previous_kernel();
+  const int M = static_cast<int>(p.Q.N), N = static_cast<int>(p.K.N), Hq = static_cast<int>(p.Q.H);
+  const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
+  const int part = static_cast<int>(blockIdx.x) % n_parts, bh = static_cast<int>(blockIdx.x) / n_parts;
+  const int b = bh / Hkv, hk = bh % Hkv;
+  const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
+  const int window = static_cast<int>(p.mask.window), n_sink = p.mask.n_sink;
+  const int first = L - nq;                           // position of row 0
+  // tiles that some row sees: those of the sinks, then those of the window
+  const int end_t = nq > 0 ? (L + 127) / 128 : 0;
+  const int sink_t = min((n_sink + 127) / 128, end_t), low_t = max(sink_t, max(0, first - window + 1) / 128);
+  const int n_tiles = sink_t + max(0, end_t - low_t), n_pairs = (n_tiles + 1) / 2;
+  const int my_pairs = part < n_pairs ? (n_pairs - part + n_parts - 1) / n_parts : 0;
+  auto tile_of = [&](int v) { return v < sink_t ? v : v - sink_t + low_t; };
+  // does group g have a tile in the CTA's pair i, and which?
+  auto has = [&](int i, int g) { return 2 * (part + i * n_parts) + g < n_tiles; };
+  auto tile_at = [&](int i, int g) { return tile_of(2 * (part + i * n_parts) + g); };
+  const int cols = pm * G, n_mma = (cols + 15) / 16 * 16, n_box = min(2, (nq + pm - 1) / pm);
+  const float* prev = p.prev ? p.prev + bh * p.prev_stride : nullptr;
+  float* mass = p.mass + bh * p.mass_stride;
+  // keys that no row sees
+  for (int64_t j = static_cast<int64_t>(part) * kWideThreads + tid; j < N; j += n_parts * kWideThreads) {
+    const int t = static_cast<int>(j >> 7);
+    if (t < sink_t || (t >= low_t && t < end_t)) continue;
+    mass[j] = j < L && prev ? p.decay * prev[j] : 0.f;
+  }
+  if (my_pairs == 0) return;
+
+  const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + 2 * C::kTile);
+  // MMA columns past the box: zero rows (the boxes never write them)
+  for (int i = tid; i < 2 * (n_mma - cols) * (D / 8); i += kWideThreads) {
+    const int c = i % (D / 8), r = cols + i / (D / 8) % (n_mma - cols), s = i / (D / 8) / (n_mma - cols);
+    *reinterpret_cast<uint4*>(smem + s * C::kTile + (c / 8) * (128 * 128) + sw128_offset(r, c % 8)) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async();
+  if (tid < 256) {                                    // -inf: the row adds nothing
+    const int c = tid & 127, r = (tid >> 7) * pm + c / G;
+    const float l = c < cols && r < nq ? p.lse[(static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + r] : -INFINITY;
+    ny[tid >> 7][c] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    abort_sh = 0;
+    mbar_init(&bar_q, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bar_k[i], 1);
+      mbar_init(&bar_kempty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_sfree[i], 8);
+    }
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  volatile int* abort_flag = &abort_sh;
+
+  if (warp == 1) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      mbar_expect_tx(&bar_q, static_cast<uint32_t>(n_box * cols * D * 2));
+      for (int x = 0; x < n_box; ++x)
+        for (int c = 0; c < D / 64; ++c)
+          tma_rows_4d(sQ + x * C::kTile + c * (128 * 128), &mq, c * 64, hk * G, x * pm, b, &bar_q);
+      int f = 0;                                      // tiles issued
+      bool ok = true;
+      for (int i = 0; ok && i < my_pairs; ++i) {
+        for (int g = 0; g < 2 && has(i, g); ++g) {
+          const int s = f % NS;
+          if (f >= NS) ok = mbar_wait_or_abort(&bar_kempty[s], (f / NS - 1) & 1, p.err, abort_flag);
+          if (!ok) break;
+          mbar_expect_tx(&bar_k[s], C::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_rows_4d(sK + s * C::kTile + c * (128 * 128), &mk, c * 64, tile_at(i, g) * 128, p.K.sH == 0 ? 0 : hk,
+                        p.K.sB == 0 ? 0 : b, &bar_k[s]);
+          ++f;
+        }
+      }
+      // no copy may be in flight when the CTA ends; without an abort the MMA
+      // role has waited for all of them
+      if (*abort_flag) {
+        mbar_wait(&bar_q, 0, p.err);
+        for (int i = max(0, f - NS); i < f; ++i) mbar_wait(&bar_k[i % NS], (i / NS) & 1, p.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- MMA
+    const uint32_t idesc = idesc_bf16(128, n_mma, false);
+    bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bar_q, 0, p.err, abort_flag));
+    int f = 0, n = 0;                                 // tiles before this pair; products per group
+    for (int i = 0; ok && i < my_pairs; ++i) {
+      const int n_g = has(i, 1) ? 2 : 1;
+      for (int x = 0; ok && x < n_box; ++x, ++n) {
+        for (int g = 0; g < n_g; ++g) {
+          const int s = (f + g) % NS, d = g * 2 + (n & 1);
+          if (x == 0) ok = mbar_wait_or_abort(&bar_k[s], ((f + g) / NS) & 1, p.err, abort_flag);
+          if (ok && n >= 2) ok = mbar_wait_or_abort(&bar_sfree[d], (n / 2 - 1) & 1, p.err, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a0 = sdesc_sw128(sK + s * C::kTile, 16, 1024);
+          const uint64_t b0 = sdesc_sw128(sQ + x * C::kTile, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (128 * 128) + (kk % 4) * 32;
+            if (elect_one())
+              mma_ss(tmem + d * 128, sdesc_add(a0, off), sdesc_add(b0, off), idesc, kk > 0 ? 1u : 0u);
+          }
+          if (elect_one()) {
+            tc_commit(&bar_s[d]);
+            if (x == n_box - 1) tc_commit(&bar_kempty[s]);
+          }
+          __syncwarp();
+        }
+      }
+      f += n_g;
+    }
+  } else {
+    // ----------------------------------------------------------- consumers
+    const int g = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1, key = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + g * 256 + half * 64 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    int n = 0;                                        // products of this group
+    // (after an abort the waits return at once; the sums are then meaningless and
+    // the error word says so)
+    for (int i = 0; i < my_pairs; ++i) {
+      if (!has(i, g)) continue;
+      const int j = tile_at(i, g) * 128 + key;
+      const float old = prev && half == 0 && j < L ? prev[j] : 0.f;
+      float sum = 0.f;
+      for (int x = 0; x < n_box; ++x, ++n) {
+        const int d = n & 1;
+        mbar_wait_or_abort(&bar_s[g * 2 + d], (n / 2) & 1, p.err, abort_flag);
+        tc_fence_after();
+        // rows of the box that see this key: c_lo <= c < c_hi
+        const int row = x * pm, at = first + row;
+        const int hi = j < n_sink ? nq - row : min(nq - row, j + window - at);
+        const int c_lo = min(pm, max(0, j - at)) * G, c_hi = j < L ? min(pm, max(0, hi)) * G : 0;
+        const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128);
+        const bool none = __all_sync(0xffffffffu, c_lo >= c_hi);
+        unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+        for (int c = half * 64; c < min(none ? 0 : n_mma, half * 64 + 64); c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tS + d * 128 + (c & 32), v);
+          if (!full) {                                // (columns past the box are past c_hi)
+            const int lo = c_lo - c, up = c_hi - c;
+            const uint32_t see = (up <= 0 ? 0u : up >= 32 ? ~0u : (1u << up) - 1u) &
+                                 ~(lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see & (1u << e))) v[e] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(&ny[x][c + e]);
+            float t0, t1, t2, t3;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, n2.x), t0, t1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, n2.y), t2, t3);
+            a2[(e / 2) & 3] = f2_add(a2[(e / 2) & 3], f2_pack(ex2(t0), ex2(t1)));
+            a2[(e / 2 + 1) & 3] = f2_add(a2[(e / 2 + 1) & 3], f2_pack(ex2(t2), ex2(t3)));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_sfree[g * 2 + d]);
+        float s0, s1, s2, s3, s4, s5, s6, s7;
+        f2_unpack(a2[0], s0, s1);
+        f2_unpack(a2[1], s2, s3);
+        f2_unpack(a2[2], s4, s5);
+        f2_unpack(a2[3], s6, s7);
+        sum += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
+      }
+      if (half == 1) group_sum[g][i & 1][key] = sum;
+      named_sync(1 + g, 256);
+      if (half == 0 && j < N) mass[j] = j < L ? fmaf(p.decay, old, sum + group_sum[g][i & 1][key]) : 0.f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -414,14 +715,19 @@ __global__ void __launch_bounds__(256) mass_join_kernel(const KeyMassParams p, c
 constexpr int kFewRows = 16;
 constexpr int kMaxParts = 8;
 
-// Parts that the query rows are cut into: enough for four CTAs per SM, at least
-// four boxes each.  More parts than that only add partial sums.
+// Query rows up to which the keys stream past resident queries (two boxes).
+int64_t mass_mid_rows(int64_t G) { return 2 * (128 / G) * G; }
+
+// Parts that the query rows are cut into: two where a CTA would run 256 boxes one
+// after the other (the first keys of a prompt are seen by all its rows), more where
+// there are fewer key tiles than SMs, at least four boxes each.  A prompt of 8192
+// takes 365, 356 and 375 us in 1, 2 and 4 parts, one of 2048 97, 55 and 40.
 int mass_parts(const TensorDesc& Q, const TensorDesc& K) {
-  const int64_t G = Q.H / K.H, tiles = (K.N + 127) / 128 * K.B * K.H;
-  if (Q.N * G <= kFewRows) return 1;
+  const int64_t G = Q.H / K.H, tiles = (K.N + 255) / 256 * K.B * K.H;
+  if (Q.N * G <= mass_mid_rows(G)) return 1;
   const int64_t boxes = (Q.N * G + 127) / 128;
-  return static_cast<int>(
-      std::max<int64_t>(1, std::min({boxes / 4, 4 * kSMs / tiles, static_cast<int64_t>(kMaxParts)})));
+  const int64_t parts = std::max(2 * kSMs / tiles, std::min<int64_t>(2, boxes / 128));
+  return static_cast<int>(std::max<int64_t>(1, std::min({parts, boxes / 4, static_cast<int64_t>(kMaxParts)})));
 }
 
 template <int D>
@@ -441,17 +747,26 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
     return launch_after(kernel, static_cast<unsigned>(BH * parts), kWarps * 32, bytes, 1, s, p, parts);
   }
   const int pm = static_cast<int>(std::min(p.Q.N, 128 / G));
-  const int parts = mass_parts(p.Q, p.K);
   CUtensorMap mq, mk;
   if (!encode_queries_map(&mq, p.Q, static_cast<int>(G), pm, 1) || !encode_keys_map(&mk, p.K, 128))
     return cudaErrorNotSupported;
+  if (rows <= mass_mid_rows(G)) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(mass_mid_kernel<D>, MidCfg<D>::kSmem, done);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = (p.K.N + 255) / 256;
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(pairs, (kSMs + BH / 2) / BH)));
+    return launch_after(mass_mid_kernel<D>, static_cast<unsigned>(BH * parts), kWideThreads, MidCfg<D>::kSmem, 1, s, p,
+                        parts, pm, mq, mk);
+  }
+  const int parts = mass_parts(p.Q, p.K);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(mass_wide_kernel<D>, MassCfg<D>::kBytes, done);
+  cudaError_t e = allow_smem(mass_wide_kernel<D>, MassCfg<D>::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (p.K.N + 127) / 128 * BH * parts;
+  const int64_t ctas = (p.K.N + 255) / 256 * BH * parts;
   if (ctas >= (1ll << 31)) return cudaErrorInvalidValue;
   double* partial = static_cast<double*>(p.ws);
-  e = launch_after(mass_wide_kernel<D>, static_cast<unsigned>(ctas), kWideThreads, MassCfg<D>::kBytes, 1, s, p, parts,
+  e = launch_after(mass_wide_kernel<D>, static_cast<unsigned>(ctas), kWideThreads, MassCfg<D>::kSmem, 1, s, p, parts,
                    pm, partial, mq, mk);
   if (e != cudaSuccess || parts == 1) return e;
   return launch_after(mass_join_kernel, static_cast<unsigned>((p.K.N + 255) / 256 * BH), 256, 0, 1, s, p, parts,
