@@ -440,8 +440,11 @@ cudaError_t run_few(const CacheAttnParams& p, const AttnParts& parts, int prefix
 }
 
 constexpr int kFewRows = 16;
-constexpr int kFewCtas = 4 * kSMs;
-constexpr int kFewKeys = 64;
+// One CTA for every place on the chip, with 128 keys each at least.  8 KV-head rows
+// of 32768 keys take 27 us in 256 CTAs, 34 in 576 (two rounds of clusters), 33 in
+// 128; 8 rows of 1024 keys 7.9 us in 64 CTAs and one kernel, 9.5 in 128 and two.
+constexpr int kFewCtas = 2 * kSMs;
+constexpr int kFewKeys = 128;
 
 // Parts that `units` independent pieces of work of at most `keys` keys are cut
 // into: enough for `ctas` CTAs, none shorter than `shortest` keys.
@@ -466,9 +469,13 @@ Plan plan(const TensorDesc& Q, const TensorDesc& K, int64_t keys, bool has_prefi
   w.few_prefix = has_prefix && Q.B * rows <= kFewRows;
   w.rank = 1;
   int own = 0, prefix = 0;
-  if (w.few_own) own = cut(K.B * K.H, keys, kFewCtas, kFewKeys, kMaxParts * kMaxRank);
-  if (w.few_prefix) prefix = cut(K.H, P, kFewCtas, kFewKeys, kMaxParts * kMaxRank);
+  const int64_t ctas = w.few_own && w.few_prefix ? kFewCtas / 2 : kFewCtas;
+  if (w.few_own) own = cut(K.B * K.H, keys, ctas, kFewKeys, kMaxParts * kMaxRank);
+  if (w.few_prefix) prefix = cut(K.H, P, ctas, kFewKeys, kMaxParts * kMaxRank);
   w.rank = power_of_two_up_to(std::min(std::max({own, prefix, 1}), kMaxRank));
+  // (clusters as large as the prefix's parts want them, but not so large that the
+  // sequences' own keys, which may want one CTA each, take more than their places)
+  while (w.rank > 1 && own < w.rank && w.few_own && K.B * K.H * w.rank > ctas) w.rank /= 2;
   w.own = w.few_own ? std::max(own / w.rank, 1) : cut(wide_units(Q, K, false), keys, kSMs, 256, kMaxParts);
   if (has_prefix)
     w.prefix = w.few_prefix ? std::max(prefix / w.rank, 1) : cut(wide_units(Q, K, true), P, kSMs, 256, kMaxParts);
@@ -489,6 +496,10 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s) {
   const bool pre = p.Kp.ptr != nullptr;
   const int64_t keys = std::min(p.K.N, p.mask.window + p.mask.n_sink + p.Q.N);
   const Plan w = plan(p.Q, p.K, keys, pre, p.Kp.N);
+  // (the workspace was sized without the window and the prefix's length, for at
+  // least as many parts)
+  const Plan most = plan(p.Q, p.K, p.K.N, pre, 1ll << 31);
+  if (w.own + w.prefix > most.own + most.prefix) return cudaErrorInvalidValue;
   AttnParts parts;
   parts.own = w.own;
   parts.prefix = w.prefix;

@@ -350,6 +350,25 @@ def test_evict(B, Hkv, d, N, budget, recent, n_sink, kv, kind):
     check_evict(mass, K, V, budget, recent, n_sink, kv)
 
 
+@pytest.mark.parametrize("levels", [1 << 30, 50])
+@pytest.mark.parametrize("B,Hkv,N,budget", [(40, 2, 41003, 9000), (3, 25, 20000, 700), (1, 1, 400000, 100001),
+                                            (1, 3, 131072, 4096)])
+def test_evict_long_caches(B, Hkv, N, budget, levels):
+    """Rows held in shared memory by one CTA or a cluster, and rows too long for it."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    mass = torch.randint(0, levels, (B, Hkv, N), generator=g, device="cuda").float()
+    K = torch.zeros((B, 1, N, 64), dtype=torch.bfloat16, device="cuda").expand(B, Hkv, N, 64)
+    keep, *_ = pbs.pbs_evict(mass, K, K, budget, 100, 4)
+    pbs.pbs_check_device()
+    x = mass.cpu().numpy()
+    always = np.zeros(N, bool)
+    always[:4] = always[N - 100:] = True
+    for b in range(B):
+        for h in range(Hkv):
+            order = np.lexsort((np.arange(N), -x[b, h].astype(np.float64), ~always))
+            assert np.array_equal(keep[b, h].cpu().numpy(), np.sort(order[:budget])), (b, h)
+
+
 def test_evict_into_larger_buffers():
     """Kept rows at the start of caches with room to grow; everything behind them stays."""
     B, Hkv, d, N, budget = 2, 2, 64, 500, 120
