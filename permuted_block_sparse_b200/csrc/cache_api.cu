@@ -25,6 +25,9 @@ int launched(cudaError_t e, const char* what) {
   return fail(PBS_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
 
+// The sizes that pbs_workspace_size gives.
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
 bool broadcast(const TensorDesc& t) { return (t.H > 1 && t.sH == 0) || (t.B > 1 && t.sB == 0); }
 
 // Queries against a cache: shapes, head groups and the mask's numbers.
@@ -90,7 +93,7 @@ int attn(const pbs_tensor* Qt, const pbs_tensor* Kpt, const pbs_tensor* Vpt, boo
     if (p.Kp.B != 1 || p.Kp.H != p.K.H || p.Kp.D != p.K.D)
       return fail(PBS_ERR_INVALID_ARG, "Kp must be [1, Hkv, P, D] with K's Hkv and D");
   }
-  if ((rc = pbs::api_check_ws(ws, ws_bytes, pbs::cache_attn_ws_bytes(p.Q, p.K, prefix)))) return rc;
+  if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::cache_attn_ws_bytes(p.Q, p.K, prefix))))) return rc;
   p.mask = mask_of(p.K, kv_len, q_len, window, n_sink);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.lse = lse;
@@ -133,7 +136,7 @@ int pbs_key_mass(const pbs_tensor* Qt, const pbs_tensor* Kt, const float* lse, c
     return fail(PBS_ERR_INVALID_ARG, "prev and mass are one buffer with two strides");
   if (prev && (!(decay >= 0.0f) || !std::isfinite(decay)))
     return fail(PBS_ERR_INVALID_ARG, "decay must be finite and >= 0");
-  if ((rc = pbs::api_check_ws(ws, ws_bytes, pbs::key_mass_ws_bytes(p.Q, p.K)))) return rc;
+  if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::key_mass_ws_bytes(p.Q, p.K))))) return rc;
   p.mask = mask_of(p.K, kv_len, q_len, window, n_sink);
   p.lse = lse;
   p.prev = prev;
@@ -172,7 +175,7 @@ int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* Kt, cons
     return fail(PBS_ERR_UNSUPPORTED, "K_out and V_out may not be broadcast views");
   if (overlap(p.Ko, p.K) || overlap(p.Ko, p.V) || overlap(p.Vo, p.K) || overlap(p.Vo, p.V) || mass == mass_out)
     return fail(PBS_ERR_INVALID_ARG, "outputs overlap inputs");
-  if ((rc = pbs::api_check_ws(ws, ws_bytes, pbs::evict_ws_bytes(p.K)))) return rc;
+  if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::evict_ws_bytes(p.K))))) return rc;
   p.mass = mass;
   p.mass_stride = mass_stride;
   p.mass_out_stride = mass_out_stride;
