@@ -10,9 +10,9 @@
 //
 // Query rows of one KV head that read the same keys run together: the G heads
 // of the group, the M new tokens and, over a shared prefix, the sequences.  Up
-// to 16 such rows (a decode step) are bound by the bytes of K and V and run in
-// attn_few_kernel below; more rows run on the tcgen05 kernel of
-// cache_attn_wide.cu.
+// to 32 such rows (a decode step) are bound by the bytes of K and V and run in
+// attn_few_kernel below, 8 or 16 rows a CTA (a second block of rows finds the keys
+// in L2); more rows run on the tcgen05 kernel of cache_attn_wide.cu.
 #include <math.h>
 
 #include <algorithm>
@@ -99,9 +99,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
   const bool pre = static_cast<int>(blockIdx.x) < prefix_ctas;
   const int cta = pre ? blockIdx.x : blockIdx.x - prefix_ctas;
   const int n_clusters = pre ? parts.prefix : parts.own, n_parts = n_clusters * n_rank;
-  const int part = cta % n_parts, unit = cta / n_parts;
+  const int rows = (pre ? static_cast<int>(p.Q.B) : 1) * M * G, n_block = (rows + NG * 8 - 1) / (NG * 8);
+  const int part = cta % n_parts, block = cta / n_parts % n_block, unit = cta / n_parts / n_block;
   const int hk = unit % Hkv, b = pre ? 0 : unit / Hkv;
-  const int R = (pre ? static_cast<int>(p.Q.B) : 1) * M * G;
+  const int row0 = block * NG * 8, R = min(NG * 8, rows - row0);     // this CTA's rows
   const int nq = pre ? M : cache_len(p.mask.q_len, b, M, p.err);
   if (nq == 0) return;
   const int L = pre ? static_cast<int>(p.Kp.N) : cache_len(p.mask.kv_len, b, p.K.N, p.err);
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
   if (tid < NG * 8) {
     FewRow f{0, -1, -1};
     if (tid < R) {
-      const int bb = pre ? tid / (M * G) : b, r = tid / G % M, h = hk * G + tid % G;
+      const int i = row0 + tid, bb = pre ? i / (M * G) : b, r = i / G % M, h = hk * G + i % G;
       const int pos = L - nq + r;
       if (pre ? r < cache_len(p.mask.q_len, bb, M, p.err) : r < nq) {
         f.out = (bb * Hq + h) * M + r;
@@ -137,9 +138,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
   uint32_t qa[D / 16][2 * NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const int i = g * 8 + lane / 4;
+    const int i = row0 + g * 8 + lane / 4;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q.ptr);
-    const bool valid = row[i].out >= 0;
+    const bool valid = row[g * 8 + lane / 4].out >= 0;
     if (valid) q += (pre ? i / (M * G) : b) * p.Q.sB + (hk * G + i % G) * p.Q.sH + i / G % M * p.Q.sN + (lane & 3) * 2;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
 constexpr int kMaxParts = 32;      // that the prefix and the own keys each leave to attn_join_kernel
 // One warp per output row, lane s looking after part s, s + 32, ...: the largest
 // maximum, then the parts' sums and accumulators rescaled to it and added in the
-// order of the parts, eight accumulator rows in flight.
+// order of the parts, sixteen accumulator rows in flight.
 template <int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const CacheAttnParams p, const AttnParts parts) {
   wait_for_previous_kernel();
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const CacheAttnParams p,
   const int64_t M = p.Q.N;
   if (out >= p.Q.B * p.Q.H * M) return;
   if (p.mask.q_len && out % M >= cache_len(p.mask.q_len, out / M / p.Q.H, M, p.err)) return;
-  constexpr int E = D / 32, kHold = (2 * kMaxParts + 31) / 32;
+  constexpr int kBatch = 16, E = D / 32, kHold = (2 * kMaxParts + 31) / 32;
   float2 ml[kHold];
   float mm = -INFINITY;
 #pragma unroll
@@ -391,10 +392,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const CacheAttnParams p,
     // (a part in which the row sees nothing has sum 0 and no accumulator)
     const float w = ml[q].y == 0.f ? 0.f : mm == -INFINITY ? 1.f : ex2(ml[q].x - mm);
     const float wl = ml[q].y == 0.f ? 0.f : w * ml[q].y;
-    for (int s0 = 0; s0 < 32 && q * 32 + s0 < n; s0 += 8) {
-      float x[8][E];
+    for (int s0 = 0; s0 < 32 && q * 32 + s0 < n; s0 += kBatch) {
+      float x[kBatch][E];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < kBatch; ++s) {
         const bool some = q * 32 + s0 + s < n && __shfl_sync(0xffffffffu, ml[q].y, s0 + s) != 0.f;
         const float* at = acc + static_cast<int64_t>(q * 32 + s0 + s) * D;
         if constexpr (E == 4) {
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const CacheAttnParams p,
         }
       }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < kBatch; ++s) {
         const float ws = __shfl_sync(0xffffffffu, w, s0 + s);
         ll += __shfl_sync(0xffffffffu, wl, s0 + s);
 #pragma unroll
@@ -439,7 +440,7 @@ cudaError_t run_few(const CacheAttnParams& p, const AttnParts& parts, int prefix
                       parts, prefix_ctas, rank);
 }
 
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 32;
 // One CTA for every place on the chip, with 128 keys each at least.  8 KV-head rows
 // of 32768 keys take 27 us in 256 CTAs, 34 in 576 (two rounds of clusters), 33 in
 // 128; 8 rows of 1024 keys 7.9 us in 64 CTAs and one kernel, 9.5 in 128 and two.
@@ -457,6 +458,9 @@ int power_of_two_up_to(int n) {
   return x;
 }
 
+// Blocks of rows that attn_few_kernel runs in different CTAs.
+int64_t row_blocks(int64_t rows) { return (rows + 15) / 16; }
+
 struct Plan {
   bool few_own, few_prefix;
   int rank;                        // CTAs per cluster of the few-row kernel
@@ -469,13 +473,14 @@ Plan plan(const TensorDesc& Q, const TensorDesc& K, int64_t keys, bool has_prefi
   w.few_prefix = has_prefix && Q.B * rows <= kFewRows;
   w.rank = 1;
   int own = 0, prefix = 0;
+  const int64_t own_units = K.B * K.H * row_blocks(rows), prefix_units = K.H * row_blocks(Q.B * rows);
   const int64_t ctas = w.few_own && w.few_prefix ? kFewCtas / 2 : kFewCtas;
-  if (w.few_own) own = cut(K.B * K.H, keys, ctas, kFewKeys, kMaxParts * kMaxRank);
-  if (w.few_prefix) prefix = cut(K.H, P, ctas, kFewKeys, kMaxParts * kMaxRank);
+  if (w.few_own) own = cut(own_units, keys, ctas, kFewKeys, kMaxParts * kMaxRank);
+  if (w.few_prefix) prefix = cut(prefix_units, P, ctas, kFewKeys, kMaxParts * kMaxRank);
   w.rank = power_of_two_up_to(std::min(std::max({own, prefix, 1}), kMaxRank));
   // (clusters as large as the prefix's parts want them, but not so large that the
   // sequences' own keys, which may want one CTA each, take more than their places)
-  while (w.rank > 1 && own < w.rank && w.few_own && K.B * K.H * w.rank > ctas) w.rank /= 2;
+  while (w.rank > 1 && own < w.rank && w.few_own && own_units * w.rank > ctas) w.rank /= 2;
   w.own = w.few_own ? std::max(own / w.rank, 1) : cut(wide_units(Q, K, false), keys, kSMs, 256, kMaxParts);
   if (has_prefix)
     w.prefix = w.few_prefix ? std::max(prefix / w.rank, 1) : cut(wide_units(Q, K, true), P, kSMs, 256, kMaxParts);
@@ -508,8 +513,11 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s) {
   parts.ml = reinterpret_cast<float2*>(parts.acc + rows * n * p.Q.D);
   const bool two = std::max(w.few_own ? p.Q.N * (p.Q.H / p.K.H) : 0,
                             w.few_prefix ? p.Q.B * p.Q.N * (p.Q.H / p.K.H) : 0) > 8;
-  const int prefix_ctas = w.few_prefix ? static_cast<int>(p.K.H) * w.prefix * w.rank : 0;
-  const int ctas = prefix_ctas + (w.few_own ? static_cast<int>(p.K.B * p.K.H) * w.own * w.rank : 0);
+  const int64_t own_rows = p.Q.N * (p.Q.H / p.K.H);
+  const int prefix_ctas =
+      w.few_prefix ? static_cast<int>(p.K.H * row_blocks(p.Q.B * own_rows)) * w.prefix * w.rank : 0;
+  const int ctas =
+      prefix_ctas + (w.few_own ? static_cast<int>(p.K.B * p.K.H * row_blocks(own_rows)) * w.own * w.rank : 0);
   cudaError_t e = cudaSuccess;
   if (pre && !w.few_prefix && (e = launch_attn_wide(p, parts, true, s)) != cudaSuccess) return e;
   if (!w.few_own && (e = launch_attn_wide(p, parts, false, s)) != cudaSuccess) return e;
