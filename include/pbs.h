@@ -334,6 +334,7 @@ int pbs_attn_fwd_ex(const pbs_tensor* Q, const pbs_tensor* K, const pbs_tensor* 
  *  - M and N are any positive lengths (no multiple of a block); Hq / Hkv is
  *    at most 64.  K and V may be broadcast views (zero batch or head
  *    strides); Q and O may not.  Hkv * B is at most 65535.
+ *  - Outputs may not overlap inputs (but see prev of pbs_key_mass).
  *  - What a row sees decides its result: NaN or infinity in a key, or in the
  *    value of a key, that the row does not see leaves it unchanged.
  *  - Two calls that may overlap in time need two workspaces, also where they

@@ -41,7 +41,7 @@ int check_pair(const TensorDesc& Q, const TensorDesc& K, int64_t window, int n_s
   if (Q.B * Q.H * Q.N >= (1ll << 31)) return fail(PBS_ERR_UNSUPPORTED, "B * Hq * M above 2^31");
   if (broadcast(Q)) return fail(PBS_ERR_UNSUPPORTED, "Q may not be a broadcast view (zero head or batch stride)");
   if (window < 0 || n_sink < 0) return fail(PBS_ERR_INVALID_ARG, "window/n_sink negative");
-  if (!(scale > 0.0f) || !std::isfinite(scale))
+  if (!(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f))
     return fail(PBS_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
   return PBS_OK;
 }
@@ -71,6 +71,12 @@ bool overlap(const TensorDesc& a, const TensorDesc& b) {
   extent(a, &al, &ah);
   extent(b, &bl, &bh);
   return al < bh && bl < ah;
+}
+
+// Rows of fp32, `stride` elements apart.
+bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
+                  int64_t rows) {
+  return a < b + (rows - 1) * b_stride + b_len && b < a + (rows - 1) * a_stride + a_len;
 }
 
 int attn(const pbs_tensor* Qt, const pbs_tensor* Kpt, const pbs_tensor* Vpt, bool prefix, const pbs_tensor* Kt,
@@ -132,8 +138,9 @@ int pbs_key_mass(const pbs_tensor* Qt, const pbs_tensor* Kt, const float* lse, c
   if (!lse || !mass) return fail(PBS_ERR_INVALID_ARG, "lse or mass is null");
   if (mass_stride < p.K.N || (prev && prev_stride < p.K.N))
     return fail(PBS_ERR_INVALID_ARG, "mass and prev rows must be at least N = %lld elements apart", (long long)p.K.N);
-  if (prev == mass && prev_stride != mass_stride)
-    return fail(PBS_ERR_INVALID_ARG, "prev and mass are one buffer with two strides");
+  if (prev && !(prev == mass && prev_stride == mass_stride) &&
+      rows_overlap(prev, prev_stride, p.K.N, mass, mass_stride, p.K.N, p.K.B * p.K.H))
+    return fail(PBS_ERR_INVALID_ARG, "prev and mass overlap without being the same");
   if (prev && (!(decay >= 0.0f) || !std::isfinite(decay)))
     return fail(PBS_ERR_INVALID_ARG, "decay must be finite and >= 0");
   if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::key_mass_ws_bytes(p.Q, p.K))))) return rc;
@@ -173,8 +180,9 @@ int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* Kt, cons
     return fail(PBS_ERR_INVALID_ARG, "mass or mass_out rows too close together");
   if (broadcast(p.Ko) || broadcast(p.Vo))
     return fail(PBS_ERR_UNSUPPORTED, "K_out and V_out may not be broadcast views");
-  if (overlap(p.Ko, p.K) || overlap(p.Ko, p.V) || overlap(p.Vo, p.K) || overlap(p.Vo, p.V) || mass == mass_out)
-    return fail(PBS_ERR_INVALID_ARG, "outputs overlap inputs");
+  if (overlap(p.Ko, p.K) || overlap(p.Ko, p.V) || overlap(p.Vo, p.K) || overlap(p.Vo, p.V) || overlap(p.Ko, p.Vo) ||
+      rows_overlap(mass, mass_stride, p.K.N, mass_out, mass_out_stride, budget, p.K.B * p.K.H))
+    return fail(PBS_ERR_INVALID_ARG, "outputs overlap inputs or each other");
   if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::evict_ws_bytes(p.K))))) return rc;
   p.mass = mass;
   p.mass_stride = mass_stride;

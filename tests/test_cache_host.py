@@ -120,6 +120,7 @@ def _window(lib, q=None, k=None, v=None, o=None, window=16, n_sink=0, scale=0.1,
     (dict(scale=0.0), -1, b"softmax_scale"),
     (dict(scale=float("nan")), -1, b"softmax_scale"),
     (dict(scale=float("inf")), -1, b"softmax_scale"),
+    (dict(scale=3e38), -1, b"softmax_scale"),
     (dict(q=_desc(B=300, H=256, N=1), k=_desc(B=300, H=256)), -2, b"65535"),
 ])
 def test_attn_window_refusals(lib, kw, code, word):
@@ -159,7 +160,7 @@ def test_key_mass_refusals(lib):
 
     for kw in (dict(lse=0), dict(mass=0), dict(s_mass=255), dict(s_prev=255), dict(decay=-1.0),
                dict(decay=float("nan")), dict(decay=float("inf")), dict(window=-1),
-               dict(prev=0x9000, s_prev=512)):
+               dict(prev=0x9000, s_prev=512), dict(prev=0x9004), dict(prev=0x9000 - 4 * 300)):
         assert call(**kw) == -1, kw
 
 
@@ -174,6 +175,7 @@ def test_evict_refusals(lib):
     for kw, code in ((dict(budget=0), -1), (dict(budget=257), -1), (dict(budget=65), -1), (dict(recent=61), -1),
                      (dict(recent=-1), -1), (dict(n_sink=-1), -1), (dict(mass=0), -1), (dict(keep=0), -1),
                      (dict(out=0), -1), (dict(s=255), -1), (dict(s_out=63), -1), (dict(out=0x2000), -1),
+                     (dict(out=0x2000 + 4 * 100), -1), (dict(vo=_desc(N=64, ptr=0x3000100)), -1),
                      (dict(ko=_desc(N=64, ptr=0x1000000)), -1), (dict(vo=_desc(N=64, ptr=0x2000100)), -1),
                      (dict(ko=_desc(H=1, N=64, ptr=0x3000000)), -1), (dict(ko=_desc(N=70, ptr=0x3000000)), -1),
                      (dict(ko=_desc(N=64, ptr=0x3000000, sH=0)), -2)):

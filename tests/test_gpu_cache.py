@@ -64,6 +64,11 @@ WINDOW_CASES = [
     (1, 1, 1, 128, 520, 520, 200, 9, None, None),
     (1, 1, 1, 64, 700, 2000, 0, 0, [1999], None),
     (2, 16, 2, 128, 64, 3001, 700, 40, [3001, 1203], [64, 61]),
+    (1, 32, 1, 128, 1, 5000, 0, 0, None, None),           # 32 rows per KV head
+    (2, 12, 2, 64, 5, 900, 333, 9, [900, 11], [5, 3]),    # 30
+    (1, 33, 1, 64, 1, 1, 0, 0, None, None),               # 33 rows, one key
+    (1, 3, 1, 128, 64, 1, 5, 1, None, None),              # a chunk over one key
+    (300, 2, 2, 64, 1, 70, 20, 2, None, None),            # more sequences than places on the chip
 ]
 
 
@@ -86,6 +91,11 @@ PREFIX_CASES = [
     (2, 3, 1, 64, 100, 129, 100, [100, 30], [100, 30]),
     (5, 64, 1, 128, 2, 1000, 300, None, None),
     (2, 4, 4, 128, 1, 5000, 2000, [2000, 0], None),
+    (3, 8, 2, 128, 1, 300, 50, [50, 0, 7], [1, 0, 1]),
+    (3, 12, 2, 64, 5, 300, 50, [50, 4, 7], [5, 0, 2]),
+    (40, 8, 1, 128, 1, 40, 1, None, None),
+    (2, 33, 1, 128, 1, 1, 3, None, None),
+    (1, 2, 2, 64, 70, 1, 70, [3], None),
 ]
 
 
@@ -276,6 +286,12 @@ MASS_CASES = [
     (1, 5, 1, 128, 61, 2001, 900, 7, None, None),
     (1, 64, 2, 64, 40, 260, 0, 0, None, None),
     (1, 1, 1, 128, 700, 1300, 500, 0, None, None),
+    (2, 4, 1, 128, 64, 1111, 100, 30, [1111, 70], [64, 9]),          # one or two boxes of rows
+    (1, 4, 2, 64, 33, 4000, 0, 0, None, None),
+    (3, 5, 1, 128, 25, 700, 300, 140, [700, 0, 25], [25, 25, 0]),
+    (1, 3, 1, 64, 90, 50, 0, 0, None, None),                         # more rows than keys
+    (1, 8, 1, 128, 600, 5000, 0, 0, None, None),                     # parts of the rows
+    (300, 2, 2, 64, 1, 70, 20, 2, None, None),
 ]
 
 
