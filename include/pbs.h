@@ -395,8 +395,9 @@ int pbs_key_mass(const pbs_tensor* Q, const pbs_tensor* K, const float* lse, con
  *   K_out, V_out: bf16 [B, Hkv, N_out, D] with N_out >= budget, the kept rows
  *     in that order; mass_out: DEVICE fp32, rows mass_out_stride (>= budget)
  *     elements apart, their mass.  Rows at and after new_len[b] are left as
- *     they were.  None of them may overlap K, V or mass; K_out and V_out may
- *     not be broadcast views.
+ *     they were (have zeros there in mass_out where pbs_key_mass is to go on
+ *     with it as keys are appended).  None of them may overlap another, K, V
+ *     or mass; K_out and V_out may not be broadcast views.
  *   ws: pbs_workspace_size(PBS_OP_EVICT, K, K, ...) bytes.                  */
 int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* K, const pbs_tensor* V,
               const int32_t* kv_len, int budget, int recent, int n_sink, int32_t* keep, int32_t* new_len,

@@ -33,7 +33,9 @@ namespace {
 //   same thread and P is effectively held in 16 bits of mantissa;
 //   O += P V   with V by ldmatrix.trans.
 // 16 query rows are two such groups: one QK^T tile, two PV tiles.
-// Bound: HBM, 4 D bytes per key.
+// Bound: HBM, 4 D bytes per key.  Measured: 64 sequences with 4100 visible keys each
+// (Hq 32, Hkv 8, D 128) 157 us, 6.9 TB/s; one sequence with 260 7.0 us, of which 2
+// are the launch and the rest one chain of load, products and joins.
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kGroup = 16;                      // keys per warp and stage
@@ -364,7 +366,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
 constexpr int kMaxParts = 32;      // that the prefix and the own keys each leave to attn_join_kernel
 // One warp per output row, lane s looking after part s, s + 32, ...: the largest
 // maximum, then the parts' sums and accumulators rescaled to it and added in the
-// order of the parts, sixteen accumulator rows in flight.
+// order of the parts, sixteen accumulator rows in flight.  2048 rows of 19 parts
+// take 7 us (20 MB read), small cases 3 to 5.
 template <int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const CacheAttnParams p, const AttnParts parts) {
   wait_for_previous_kernel();

@@ -12,7 +12,10 @@
 // consecutive positions a lane.
 // Masses share their leading digits, so lanes meet on the same bin: there are four
 // copies of the histogram, by lane.
+// Bound: instructions, about 0.4 us per 1024 keys and CTA behind a fixed 7 us (three
+// digits of a few barriers each).  Measured: 128 rows of 16384 to 32768 keys 23 us.
 // The gather copies the kept rows of K and V, bound by HBM: 2 x 4 D bytes a row.
+// Measured: 128 x 4097 rows of D = 128 91 us, 5.9 TB/s.
 #include <math.h>
 
 #include <algorithm>

@@ -33,7 +33,8 @@ __device__ __forceinline__ void write_mass(const KeyMassParams& p, int64_t bh, i
 // them as the A operand of m16n8k16 (keys x rows); the queries stay in registers
 // as the B operand.  A CTA's rounds of 64 keys are spread over the cache, so
 // that the keys outside a window, which are not loaded, fall on all CTAs alike.
-// Bound: HBM, 2 D bytes per visible key.
+// Bound: HBM, 2 D bytes per visible key.  Measured: 32 sequences of 4096 to 8192 keys
+// (Hq 32, Hkv 8, D 128) 72 us, 5.9 TB/s.
 // Sixteen warps per SM (four CTAs of 48 KB) hide the chain from a group's arrival
 // to its sums; with eight the schedulers issued in 41% of the cycles.
 constexpr int kWarps = 4;
@@ -184,7 +185,10 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
 //   warp 1  loads K once and the query boxes and their lse into rings of four;
 //   warps 2-17 copy K into tensor memory, then take 2^(x - y) of every column and
 //     sum it: a thread has one key and 64 of the 128 columns.
-// Bound: exponentials, 16 per clock and SM on the SFU.
+// Bound: exponentials, 16 per clock and SM on the SFU.  Measured: a prompt of 8192
+// (Hq 32, Hkv 8, D 128) 356 us, 3.0 T weights/s, of which the SFU needs 231; the
+// products and hand-offs alone take 286.  A ring of four buffers with K in shared
+// memory takes 396, products of 64 columns 458.
 constexpr int kWideThreads = 576;
 constexpr int kConsumerWarps = 16;
 constexpr int kQStages = 4;
@@ -481,7 +485,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
 // and the key tiles stream past, through a ring of four, in pairs that two groups of
 // eight consumer warps take.  Each group has two tensor-memory buffers.  CTAs are
 // one per SM; those of one (sequence, KV head) share its visible tiles in turn.
-// Bound: HBM for the keys, with many rows the exponentials.
+// Bound: HBM for the keys, with many rows the exponentials.  Measured: 61 rows of two
+// sequences (3 heads a group, D 64) over 9061 visible of 20011 keys 17 us.
 constexpr int kKStages = 4;
 
 template <int D>
