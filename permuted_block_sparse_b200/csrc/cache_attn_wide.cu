@@ -516,7 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     }
     // ---- epilogue
     if (h < n_slot) {
-      bool ok = k == 0 || mbar_wait_or_abort(&sh.bar_o[h], 0, p.err, abort_flag);
+      // (also where the slot has had no tile: the staging below overwrites tiles that
+      // the other slot's MMAs read, and Q may still be landing)
+      bool ok = mbar_wait_or_abort(&sh.bar_o[h], 0, p.err, abort_flag);
       tc_fence_after();
       // the row's sum over both halves (the maxima of both parities may still be
       // read: a barrier before and after)

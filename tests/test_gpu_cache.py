@@ -207,6 +207,19 @@ def test_rows_that_see_nothing(case):
         assert float(m.sum()) == pytest.approx(Hq * sum(min(M, x) for x in kv), rel=1e-4)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hkv,G,M,N,kv,ql", [(1, 64, 4, 40, 2, 4), (2, 7, 369, 149, 44, 251), (1, 7, 369, 149, 103, 245),
+                                             (1, 1, 256, 60, 50, 256)])
+def test_tiles_without_a_visible_key_beside_others(Hkv, G, M, N, kv, ql, d):
+    """Of the two row tiles that run together the first may see no key at all; its
+    rows are zeros and the second's are right, every time."""
+    for seed in range(12):
+        Q, K, V = inputs(60 + seed, 1, Hkv * G, Hkv, d, M, N)
+        out = torch.full_like(Q, 3.0)
+        check_window(Q, K, V, 0, 0, [kv], [ql], out=out, what=f"seed {seed}")
+        assert (out[0, :, :ql - kv] == 0).all() and (out[0, :, ql:] == 3.0).all()
+
+
 @pytest.mark.parametrize("case", SMALL_AND_LARGE, ids=str)
 def test_large_logits_and_scale(case):
     B, Hq, Hkv, d, M, N, window, n_sink = case
