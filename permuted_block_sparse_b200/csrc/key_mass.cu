@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
 //   warps 2-17 copy K into tensor memory, then take 2^(x - y) of every column and
 //     sum it: a thread has one key and 64 of the 128 columns.
 // Bound: exponentials, 16 per clock and SM on the SFU.  Measured: a prompt of 8192
-// (Hq 32, Hkv 8, D 128) 356 us, 3.0 T weights/s, of which the SFU needs 231; the
-// products and hand-offs alone take 286.  A ring of four buffers with K in shared
+// (Hq 32, Hkv 8, D 128) 347 us, 3.1 T weights/s, of which the SFU needs 231; the
+// products and hand-offs alone take 288.  A ring of four buffers with K in shared
 // memory takes 396, products of 64 columns 458.
 constexpr int kWideThreads = 576;
 constexpr int kConsumerWarps = 16;
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
   const int part = static_cast<int>(blockIdx.x) % n_parts, rest = static_cast<int>(blockIdx.x) / n_parts;
   const int bh = rest % BH, j0 = rest / BH * 256, b = bh / Hkv, hk = bh % Hkv;
   const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
-  const int64_t window = p.mask.window, first = L - nq;
-  const int n_sink = p.mask.n_sink;
+  const int window = static_cast<int>(p.mask.window), n_sink = p.mask.n_sink;
+  const int64_t first = L - nq;
   // query rows that see some key of these tiles: r0 <= r < r1, then this part's boxes of pm positions
   const int64_t last_key = min(j0 + 255, L - 1);
   int64_t r0 = max(static_cast<int64_t>(0), j0 - first), r1 = nq;
@@ -421,10 +421,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
       mbar_wait_or_abort(&bar_s[d], (u / 3) & 1, p.err, abort_flag);
       tc_fence_after();
       // rows of the box that see this key: c_lo <= c < c_hi
-      const int64_t row = r0 + static_cast<int64_t>(x) * pm, at = first + row;
-      const int64_t hi = j < n_sink ? nq - row : min(nq - row, j + window - at);
-      const int c_lo = static_cast<int>(min(static_cast<int64_t>(pm), max(static_cast<int64_t>(0), j - at))) * G;
-      const int c_hi = j < L ? static_cast<int>(min(static_cast<int64_t>(pm), max(static_cast<int64_t>(0), hi))) * G : 0;
+      // (32 bits: at >= j0 from row r0 on, so -N <= j - at < 256 and window <= N)
+      const int row = static_cast<int>(r0) + x * pm, at = static_cast<int>(first) + row;
+      const int ahead = static_cast<int>(j) - at;
+      const int hi = j < n_sink ? nq - row : min(nq - row, ahead + window);
+      const int c_lo = min(pm, max(0, ahead)) * G, c_hi = j < L ? min(pm, max(0, hi)) * G : 0;
       const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128);
       const bool none = __all_sync(0xffffffffu, c_lo >= c_hi);
       unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
@@ -656,8 +657,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
         tc_fence_after();
         // rows of the box that see this key: c_lo <= c < c_hi
         const int row = x * pm, at = first + row;
-        const int hi = j < n_sink ? nq - row : min(nq - row, j + window - at);
-        const int c_lo = min(pm, max(0, j - at)) * G, c_hi = j < L ? min(pm, max(0, hi)) * G : 0;
+        const int ahead = j - at;                     // at most 128 + 256, before the window is added
+        const int hi = j < n_sink ? nq - row : min(nq - row, ahead + window);
+        const int c_lo = min(pm, max(0, ahead)) * G, c_hi = j < L ? min(pm, max(0, hi)) * G : 0;
         const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128);
         const bool none = __all_sync(0xffffffffu, c_lo >= c_hi);
         unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
@@ -726,7 +728,7 @@ int64_t mass_mid_rows(int64_t G) { return 2 * (128 / G) * G; }
 // Parts that the query rows are cut into: two where a CTA would run 256 boxes one
 // after the other (the first keys of a prompt are seen by all its rows), more where
 // there are fewer key tiles than SMs, at least four boxes each.  A prompt of 8192
-// takes 365, 356 and 375 us in 1, 2 and 4 parts, one of 2048 97, 55 and 40.
+// takes 358, 349 and 367 us in 1, 2 and 4 parts, one of 2048 95, 54 and 39.
 int mass_parts(const TensorDesc& Q, const TensorDesc& K) {
   const int64_t G = Q.H / K.H, tiles = (K.N + 255) / 256 * K.B * K.H;
   if (Q.N * G <= mass_mid_rows(G)) return 1;
