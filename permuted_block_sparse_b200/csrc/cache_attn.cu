@@ -12,7 +12,9 @@
 // of the group, the M new tokens and, over a shared prefix, the sequences.  Up
 // to 32 such rows (a decode step) are bound by the bytes of K and V and run in
 // attn_few_kernel below, 8 or 16 rows a CTA (a second block of rows finds the keys
-// in L2); more rows run on the tcgen05 kernel of cache_attn_wide.cu.
+// in L2); more rows run on the tcgen05 kernel of cache_attn_wide.cu.  With a prefix
+// of many rows the two kernels run side by side: one is bound by products, the other
+// by HBM.
 #include <math.h>
 
 #include <algorithm>
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int M = static_cast<int>(p.Q.N), Hq = static_cast<int>(p.Q.H), Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
 
-  wait_for_previous_kernel();
+  begin_in(parts.order);
 
   // this CTA's rows and keys
   const bool pre = static_cast<int>(blockIdx.x) < prefix_ctas;
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
   const int hk = unit % Hkv, b = pre ? 0 : unit / Hkv;
   const int row0 = block * NG * 8, R = min(NG * 8, rows - row0);     // this CTA's rows
   const int nq = pre ? M : cache_len(p.mask.q_len, b, M, p.err);
-  if (nq == 0) return;
+  if (nq == 0) return end_in(parts.order);
   const int L = pre ? static_cast<int>(p.Kp.N) : cache_len(p.mask.kv_len, b, p.K.N, p.err);
   const KeyRun run = pre ? KeyRun{0, 0, 0, L} : key_run<1>(L - nq, L - 1, p.mask.window, p.mask.n_sink);
   if (tid < NG * 8) {
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
       if (c == 0) sm_ml[i] = make_float2(mm, ll);
     }
   }
-  if (n_rank == 1) return;
+  if (n_rank == 1) return end_in(parts.order);
   // ---- join the cluster: each CTA takes every n_rank-th piece of the rows
   cluster_sync_all();
   const uint32_t so_s = smem_u32(so), ml_s = smem_u32(sm_ml);
@@ -360,6 +362,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
     leave_row4(p, parts, n_slots, slot, row[i].out, c, D, acc, mm, ll);
   }
   cluster_sync_all();                             // the others may still read this CTA's shared memory
+  end_in(parts.order);
 }
 
 // ---------------------------------------------------------------- joining
@@ -449,6 +452,9 @@ constexpr int kFewRows = 32;
 // 128; 8 rows of 1024 keys 7.9 us in 64 CTAs and one kernel, 9.5 in 128 and two.
 constexpr int kFewCtas = 2 * kSMs;
 constexpr int kFewKeys = 128;
+// ... and 512 beside attn_wide_kernel, which takes longer than such a part: 17
+// sequences of 333 keys over 10007 (5 rows, D 64) take 21.7 us, 25.9 with 128.
+constexpr int kBesideKeys = 512;
 
 // Parts that `units` independent pieces of work of at most `keys` keys are cut
 // into: enough for `ctas` CTAs, none shorter than `shortest` keys.
@@ -464,6 +470,24 @@ int power_of_two_up_to(int n) {
 // Blocks of rows that attn_few_kernel runs in different CTAs.
 int64_t row_blocks(int64_t rows) { return (rows + 15) / 16; }
 
+// Parts of a prefix that attn_wide_kernel takes (one CTA of the `units` each) while
+// attn_few_kernel streams the sequences' own keys on the other SMs: the most, up to
+// `most`, that leave those `blocks` of 16 rows enough SM time, by what the two take
+// alone: 15 us and 2 us for every 128 keys of the prefix; 1 us and 0.9 us for 128
+// own keys of D 128, with more than 8 rows 2.5 times that.  The lengths are not
+// known here, only the most that they may be, so the prefix keeps half the SMs at
+// least.  64 sequences (Hq 32, Hkv 8, D 128), 1024 keys over 32768: 79 to 84 us in
+// 10 to 12 parts, 101 in all 18; 9 sequences, 4096 over 32768: 63 in 12 parts, 94 in
+// 18; D 64, 256 over 32768: 53 in 16 parts, 57 in 18.
+int beside_own(int most, bool few_own, int64_t units, int64_t P, int64_t blocks, int64_t rows, int64_t keys,
+               int64_t D) {
+  if (!few_own) return most;
+  const double own = static_cast<double>(blocks) * (0.9 * keys / 128 + 1) * D / 128 * (rows > 8 ? 2.5 : 1);
+  int parts = most;
+  while (parts > (most + 1) / 2 && own > (kSMs - units * parts) * (15 + 2 * (P / 128.0) / parts)) --parts;
+  return parts;
+}
+
 struct Plan {
   bool few_own, few_prefix;
   int rank;                        // CTAs per cluster of the few-row kernel
@@ -478,7 +502,8 @@ Plan plan(const TensorDesc& Q, const TensorDesc& K, int64_t keys, bool has_prefi
   int own = 0, prefix = 0;
   const int64_t own_units = K.B * K.H * row_blocks(rows), prefix_units = K.H * row_blocks(Q.B * rows);
   const int64_t ctas = w.few_own && w.few_prefix ? kFewCtas / 2 : kFewCtas;
-  if (w.few_own) own = cut(own_units, keys, ctas, kFewKeys, kMaxParts * kMaxRank);
+  const int shortest = has_prefix && !w.few_prefix ? kBesideKeys : kFewKeys;
+  if (w.few_own) own = cut(own_units, keys, ctas, shortest, kMaxParts * kMaxRank);
   if (w.few_prefix) prefix = cut(prefix_units, P, ctas, kFewKeys, kMaxParts * kMaxRank);
   w.rank = power_of_two_up_to(std::min(std::max({own, prefix, 1}), kMaxRank));
   // (clusters as large as the prefix's parts want them, but not so large that the
@@ -486,7 +511,9 @@ Plan plan(const TensorDesc& Q, const TensorDesc& K, int64_t keys, bool has_prefi
   while (w.rank > 1 && own < w.rank && w.few_own && own_units * w.rank > ctas) w.rank /= 2;
   w.own = w.few_own ? std::max(own / w.rank, 1) : cut(wide_units(Q, K, false), keys, kSMs, 256, kMaxParts);
   if (has_prefix)
-    w.prefix = w.few_prefix ? std::max(prefix / w.rank, 1) : cut(wide_units(Q, K, true), P, kSMs, 256, kMaxParts);
+    w.prefix = w.few_prefix ? std::max(prefix / w.rank, 1)
+                            : beside_own(cut(wide_units(Q, K, true), P, kSMs, 256, kMaxParts), w.few_own,
+                                         wide_units(Q, K, true), P, own_units, rows, keys, Q.D);
   return w;
 }
 
@@ -511,6 +538,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s) {
   AttnParts parts;
   parts.own = w.own;
   parts.prefix = w.prefix;
+  parts.order = Order::kAlone;
   const int64_t rows = p.Q.B * p.Q.H * p.Q.N, n = w.own + w.prefix;
   parts.acc = static_cast<float*>(p.ws);
   parts.ml = reinterpret_cast<float2*>(parts.acc + rows * n * p.Q.D);
@@ -522,7 +550,11 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, cudaStream_t s) {
   const int ctas =
       prefix_ctas + (w.few_own ? static_cast<int>(p.K.B * p.K.H * row_blocks(own_rows)) * w.own * w.rank : 0);
   cudaError_t e = cudaSuccess;
-  if (pre && !w.few_prefix && (e = launch_attn_wide(p, parts, true, s)) != cudaSuccess) return e;
+  if (pre && !w.few_prefix) {
+    parts.order = Order::kFirst;
+    if ((e = launch_attn_wide(p, parts, true, s)) != cudaSuccess) return e;
+    parts.order = Order::kSecond;
+  }
   if (!w.few_own && (e = launch_attn_wide(p, parts, false, s)) != cudaSuccess) return e;
   if (ctas > 0) {
     auto run = p.Q.D == 128 ? (two ? run_few<128, 2> : run_few<128, 1>) : (two ? run_few<64, 2> : run_few<64, 1>);

@@ -14,6 +14,7 @@ struct AttnParts {
   int prefix, own;
   float* acc;
   float2* ml;
+  Order order;                     // of the kernel that gets this
 };
 
 // Four columns of output row `out`, and with the first ones its lse.

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
   const int M = static_cast<int>(p.Q.N), Hq = static_cast<int>(p.Q.H), Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
   const int B = static_cast<int>(p.Q.B);
 
-  wait_for_previous_kernel();
+  begin_in(parts.order);
 
   // ---- this CTA's work: a pair of tiles, a KV head (and sequence), a part of the keys
   const int n_parts = prefix ? parts.prefix : parts.own;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     return (prefix ? (n_pos_tiles == 1 ? 0 : t % n_pos_tiles) : t) * wr.pos_per_tile;
   };
   auto has_rows = [&](int h) { return 2 * pair + h < wr.tiles && tile_row(h) < nq_own; };
-  if (!has_rows(0)) return;                           // (slot 1 then has none either)
+  if (!has_rows(0)) return end_in(parts.order);   // (slot 1 then has none either)
   const int n_slot = has_rows(1) ? 2 : 1;
   // positions of the slots' first and last rows (own keys)
   auto first_pos = [&](int h) { return L - nq_own + tile_row(h); };
@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  end_in(parts.order);
 }
 
 template <int D>

@@ -16,6 +16,20 @@ constexpr int kSMs = 148;   // B200
 // anything.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Two kernels that need nothing of each other run side by side: the first lets the
+// next one start once everything before both is done, and the second, which
+// therefore need not wait before it reads, waits for the first before its last CTA
+// ends (one CTA is enough, and the places of the others come free), so that the one
+// after them finds both done.
+enum class Order { kAlone, kFirst, kSecond };
+__device__ __forceinline__ void begin_in(Order order) {
+  if (order != Order::kSecond) wait_for_previous_kernel();
+  if (order == Order::kFirst) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void end_in(Order order) {
+  if (order == Order::kSecond && blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y) wait_for_previous_kernel();
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s,
                          Args&&... args) {

@@ -506,3 +506,51 @@ def test_streams_and_graphs(M):
         for o, want in zip(outs, (alone[i], alone[1 - i])):
             assert all(torch.equal(a, b) for a, b in zip(o, want))
     pbs.pbs_check_device()
+
+
+@pytest.mark.parametrize("B,M,d,P,N,ql", [
+    (12, 1, 128, 5000, 900, None), (40, 1, 64, 1500, 300, None), (70, 1, 128, 900, 130, None),   # tiles beside rows
+    (17, 5, 64, 3001, 333, [5, 0, 3] * 5 + [1, 0]), (12, 1, 128, 700, 400, [0] * 12),             # (the last ends at once)
+    (4, 20, 128, 3000, 800, None), (5, 33, 64, 1111, 257, [33, 1, 0, 20, 0]),                     # tiles beside tiles
+])
+@pytest.mark.parametrize("graph", [False, True])
+def test_prefix_beside_own_keys(graph, B, M, d, P, N, ql):
+    """The prefix's kernel and the sequences' own run side by side: calls whose
+    inputs the stream rewrites right before and right after them, the lengths and
+    the workspace included, give the bits of calls made alone."""
+    Hq, Hkv = 8, 2
+    sets = []
+    for i in range(3):
+        Q, K, V = inputs(300 + 10 * i, B, Hq, Hkv, d, M, N)
+        kv = torch.randint(0, N + 1, (B,), generator=torch.Generator().manual_seed(i), dtype=torch.int32).cuda()
+        sets.append((Q, rand(7 + i, 1, Hkv, P, d), rand(17 + i, 1, Hkv, P, d), K, V, kv))
+    q_len = lens(ql)
+    held = [t.clone() for t in sets[0]]
+    outs = [(torch.full_like(held[0], 7.0), torch.full((B, Hq, M), 7.0, device="cuda")) for _ in range(12)]
+
+    def step(x, out):
+        pbs.pbs_attn_prefix(*x[:5], kv_len=x[5], q_len=q_len, out=out[0], lse=out[1])
+
+    def run():
+        for i, out in enumerate(outs):
+            for t, x in zip(held, sets[i % 3]):
+                t.copy_(x)
+            step(held, out)
+
+    alone = [(torch.full_like(o, 7.0), torch.full_like(l, 7.0)) for o, l in outs[:3]]
+    for x, out in zip(sets, alone):
+        step(x, out)
+        torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        run = g.replay
+    for _ in range(5):
+        for o, l in outs:
+            o.fill_(7.0), l.fill_(7.0)
+        run()
+        torch.cuda.synchronize()
+        for i, (o, l) in enumerate(outs):
+            assert torch.equal(o, alone[i % 3][0]) and torch.equal(l, alone[i % 3][1]), i
+    pbs.pbs_check_device()
