@@ -762,7 +762,7 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
     const cudaError_t e = allow_smem(mass_mid_kernel<D>, MidCfg<D>::kSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t pairs = (p.K.N + 255) / 256;
-    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(pairs, (kSMs + BH / 2) / BH)));
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(pairs, kSMs / BH)));
     return launch_after(mass_mid_kernel<D>, static_cast<unsigned>(BH * parts), kWideThreads, MidCfg<D>::kSmem, 1, s, p,
                         parts, pm, mq, mk);
   }
