@@ -3,10 +3,10 @@
 // x_rj = scale log2(e) Q[r].K[j], y_r = log2(e) lse[r], over the query rows of
 // all heads of a KV head.  Products and exponentials in fp32; the weights of up
 // to 128 rows are added in fp32, those sums in fp64 (a prompt adds tens of
-// thousands of small terms to one key).  No atomics: a key's sum has one owner,
-// or parts that a second kernel adds in order.
+// thousands of small terms to one key), or in fp32 where there are at most eight.
+// No atomics: a key's sum has one owner, or parts that a second kernel adds in order.
 //
-// The keys are the rows of the MMA in both kernels (S^T = K Q^T), so that a
+// The keys are the rows of the MMA in all kernels (S^T = K Q^T), so that a
 // thread's values belong to one key and are summed in registers.
 #include <math.h>
 
@@ -481,13 +481,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
 }
 
 // ---------------------------------------------------------- some hundred rows
-// Up to 256 query rows per KV head (drafted tokens, the last rows of a prompt).  The
-// other way round: the queries (one or two boxes) and their lse stay in shared memory
-// and the key tiles stream past, through a ring of four, in pairs that two groups of
-// eight consumer warps take.  Each group has two tensor-memory buffers.  CTAs are
-// one per SM; those of one (sequence, KV head) share its visible tiles in turn.
-// Bound: HBM for the keys, with many rows the exponentials.  Measured: 61 rows of two
-// sequences (3 heads a group, D 64) over 9061 visible of 20011 keys 17 us.
+// 256 query rows per KV head (drafted tokens, the last rows of a prompt) and, in up to
+// four launches that each add to the one before, 1024 over many keys.  The other way
+// round: the queries (one or two boxes) and their lse stay in shared memory and the
+// key tiles stream past, through a ring of four, in pairs that two groups of eight
+// consumer warps take.  Each group has two tensor-memory buffers.  CTAs are one per
+// SM; those of one (sequence, KV head) share its visible tiles in turn.
+// Bound: HBM for the keys, with many rows the exponentials and the products, which
+// read both operands from shared memory.  Measured: 61 rows of two sequences (3 heads a
+// group, D 64) over 9061 visible of 20011 keys 13 us; 256 rows (8 KV heads, D 128) over
+// 32768 keys 33 us.
 constexpr int kKStages = 4;
 
 template <int D>
@@ -499,7 +502,7 @@ struct MidCfg {
 
 template <int D>
 __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMassParams p, const int n_parts,
-                                                                   const int pm,
+                                                                   const int pm, const int base,
                                                                    const __grid_constant__ CUtensorMap mq,
                                                                    const __grid_constant__ CUtensorMap mk) {
   using C = MidCfg<D>;
@@ -518,9 +521,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
   const int Hkv = static_cast<int>(p.K.H), G = Hq / Hkv;
   const int part = static_cast<int>(blockIdx.x) % n_parts, bh = static_cast<int>(blockIdx.x) / n_parts;
   const int b = bh / Hkv, hk = bh % Hkv;
-  const int nq = cache_len(p.mask.q_len, b, M, p.err), L = cache_len(p.mask.kv_len, b, N, p.err);
+  // this launch's query rows: from row `base`
+  const int nq_all = cache_len(p.mask.q_len, b, M, p.err), nq = min(2 * pm, max(0, nq_all - base));
+  const int L = cache_len(p.mask.kv_len, b, N, p.err);
   const int window = static_cast<int>(p.mask.window), n_sink = p.mask.n_sink;
-  const int first = L - nq;                           // position of row 0
+  const int first = L - nq_all + base;                // position of row `base`
   // tiles that some row sees: those of the sinks, then those of the window
   const int end_t = nq > 0 ? (L + 127) / 128 : 0;
   const int sink_t = min((n_sink + 127) / 128, end_t), low_t = max(sink_t, max(0, first - window + 1) / 128);
@@ -551,7 +556,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
   fence_proxy_async();
   if (tid < 256) {                                    // -inf: the row adds nothing
     const int c = tid & 127, r = (tid >> 7) * pm + c / G;
-    const float l = c < cols && r < nq ? p.lse[(static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + r] : -INFINITY;
+    const int64_t at = (static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + base + r;
+    const float l = c < cols && r < nq ? p.lse[at] : -INFINITY;
     ny[tid >> 7][c] = l == -INFINITY ? -INFINITY : -l * kLog2e;
   }
   if (warp == 0) {
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
       mbar_expect_tx(&bar_q, static_cast<uint32_t>(n_box * cols * D * 2));
       for (int x = 0; x < n_box; ++x)
         for (int c = 0; c < D / 64; ++c)
-          tma_rows_4d(sQ + x * C::kTile + c * (128 * 128), &mq, c * 64, hk * G, x * pm, b, &bar_q);
+          tma_rows_4d(sQ + x * C::kTile + c * (128 * 128), &mq, c * 64, hk * G, base + x * pm, b, &bar_q);
       int f = 0;                                      // tiles issued
       bool ok = true;
       for (int i = 0; ok && i < my_pairs; ++i) {
@@ -722,8 +728,17 @@ __global__ void __launch_bounds__(256) mass_join_kernel(const KeyMassParams p, c
 constexpr int kFewRows = 16;
 constexpr int kMaxParts = 8;
 
-// Query rows up to which the keys stream past resident queries (two boxes).
-int64_t mass_mid_rows(int64_t G) { return 2 * (128 / G) * G; }
+// Launches of mass_mid_kernel, two boxes of query rows each, that take all rows, or
+// 0 where mass_wide_kernel does: more than one launch where that kernel's key tiles
+// would take several rounds of CTAs, each with its set-up, and at most four (sums of
+// a launch are fp32).  512 rows over 32768 keys (8 KV heads, D 128) take 64 us in two
+// launches, 85 there; 1024 rows of 8 sequences over 8192 233 in four, 256 there; but
+// 400 rows over 2 x 2048 15.6 in two, 12.9 there.
+int mid_launches(const TensorDesc& Q, const TensorDesc& K) {
+  const int64_t per = 2 * (128 / (Q.H / K.H)), n = (Q.N + per - 1) / per;
+  const bool rounds = (K.N + 255) / 256 * K.B * K.H > kSMs;
+  return n == 1 || (rounds && n <= 4) ? static_cast<int>(n) : 0;
+}
 
 // Parts that the query rows are cut into: two where a CTA would run 256 boxes one
 // after the other (the first keys of a prompt are seen by all its rows), more where
@@ -731,7 +746,7 @@ int64_t mass_mid_rows(int64_t G) { return 2 * (128 / G) * G; }
 // takes 358, 349 and 367 us in 1, 2 and 4 parts, one of 2048 95, 54 and 39.
 int mass_parts(const TensorDesc& Q, const TensorDesc& K) {
   const int64_t G = Q.H / K.H, tiles = (K.N + 255) / 256 * K.B * K.H;
-  if (Q.N * G <= mass_mid_rows(G)) return 1;
+  if (mid_launches(Q, K) > 0) return 1;
   const int64_t boxes = (Q.N * G + 127) / 128;
   const int64_t parts = std::max(2 * kSMs / tiles, std::min<int64_t>(2, boxes / 128));
   return static_cast<int>(std::max<int64_t>(1, std::min({parts, boxes / 4, static_cast<int64_t>(kMaxParts)})));
@@ -757,14 +772,22 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
   CUtensorMap mq, mk;
   if (!encode_queries_map(&mq, p.Q, static_cast<int>(G), pm, 1) || !encode_keys_map(&mk, p.K, 128))
     return cudaErrorNotSupported;
-  if (rows <= mass_mid_rows(G)) {
+  if (mid_launches(p.Q, p.K) > 0) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(mass_mid_kernel<D>, MidCfg<D>::kSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t pairs = (p.K.N + 255) / 256;
     const int parts = static_cast<int>(std::max<int64_t>(1, std::min(pairs, kSMs / BH)));
-    return launch_after(mass_mid_kernel<D>, static_cast<unsigned>(BH * parts), kWideThreads, MidCfg<D>::kSmem, 1, s, p,
-                        parts, pm, mq, mk);
+    KeyMassParams q = p;
+    for (int base = 0; base < p.Q.N; base += 2 * pm) {
+      const cudaError_t e = launch_after(mass_mid_kernel<D>, static_cast<unsigned>(BH * parts), kWideThreads,
+                                         MidCfg<D>::kSmem, 1, s, q, parts, pm, base, mq, mk);
+      if (e != cudaSuccess) return e;
+      q.prev = p.mass;                                // the rows so far
+      q.prev_stride = p.mass_stride;
+      q.decay = 1.0f;
+    }
+    return cudaSuccess;
   }
   const int parts = mass_parts(p.Q, p.K);
   static std::atomic<uint64_t> done{0};

@@ -305,6 +305,11 @@ MASS_CASES = [
     (1, 3, 1, 64, 90, 50, 0, 0, None, None),                         # more rows than keys
     (1, 8, 1, 128, 600, 5000, 0, 0, None, None),                     # parts of the rows
     (300, 2, 2, 64, 1, 70, 20, 2, None, None),
+    (40, 8, 4, 64, 200, 300, 0, 0, None, None),                      # several launches, each adding to the last
+    (75, 8, 2, 128, 150, 200, 70, 9, [200, 0, 150, 31, 199] * 15, [150, 0, 64, 65, 128] * 15),
+    (1, 8, 4, 128, 512, 9500, 3000, 5, None, None),
+    (38, 5, 1, 64, 151, 1100, 0, 0, None, [151, 50, 51, 100, 1, 150, 0] * 5 + [2, 3, 101]),
+    (37, 10, 2, 128, 60, 500, 0, 0, None, None),                     # ... and the most tiles of one launch
 ]
 
 
