@@ -149,7 +149,7 @@ int pbs_key_mass(const pbs_tensor* Qt, const pbs_tensor* Kt, const float* lse, c
   p.prev = prev;
   p.prev_stride = prev_stride;
   p.mass_stride = mass_stride;
-  p.decay = decay;
+  p.decay = prev ? decay : 1.0f;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.mass = mass;
   p.ws = ws;

@@ -336,6 +336,15 @@ def test_key_mass(case, decay):
         assert torch.equal(out, got) and (room[..., N:] == -1.0).all()
 
 
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_key_mass_without_earlier_mass_ignores_decay(M):
+    Q, K, V = inputs(8, 2, 4, 2, 64, M, 400)
+    _, lse = pbs.pbs_attn_window(Q, K, V)
+    want = pbs.pbs_key_mass(Q, K, lse)
+    for decay in (0.5, NAN, INF, -1.0):
+        assert torch.equal(pbs.pbs_key_mass(Q, K, lse, None, decay), want), decay
+
+
 def test_key_mass_repeats_bit_for_bit():
     Q, K, _ = inputs(5, 2, 8, 2, 128, 500, 3000)
     lse = torch.full((2, 8, 500), 9.0, device="cuda")
