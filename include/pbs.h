@@ -397,7 +397,8 @@ int pbs_key_mass(const pbs_tensor* Q, const pbs_tensor* K, const float* lse, con
  *     elements apart, their mass.  Rows at and after new_len[b] are left as
  *     they were (have zeros there in mass_out where pbs_key_mass is to go on
  *     with it as keys are appended).  None of them may overlap another, K, V
- *     or mass; K_out and V_out may not be broadcast views.
+ *     or mass (views of one buffer that share no element are taken where
+ *     their strides agree); K_out and V_out may not be broadcast views.
  *   ws: pbs_workspace_size(PBS_OP_EVICT, K, K, ...) bytes.                  */
 int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* K, const pbs_tensor* V,
               const int32_t* kv_len, int budget, int recent, int n_sink, int32_t* keep, int32_t* new_len,

@@ -1,9 +1,11 @@
 // C-ABI entry points of the cache operators (pbs_attn_window,
 // pbs_attn_prefix, pbs_key_mass, pbs_evict): argument checks and launches.
 // See include/pbs.h for their contracts.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "pbs_internal.h"
 
@@ -61,22 +63,60 @@ pbs::CacheMask mask_of(const TensorDesc& K, const int32_t* kv_len, const int32_t
   return m;
 }
 
-// First and one-past-last byte that a tensor's elements touch.
-void extent(const TensorDesc& t, uintptr_t* lo, uintptr_t* hi) {
-  *lo = reinterpret_cast<uintptr_t>(t.ptr);
-  *hi = *lo + 2 * static_cast<uintptr_t>((t.B - 1) * t.sB + (t.H - 1) * t.sH + (t.N - 1) * t.sN + t.D);
+// One axis of two arrays of elements: sizes and strides (in elements) in each.
+struct Axis {
+  int64_t n_a, n_b, s_a, s_b;
+};
+
+// Do arrays over axes of the same strides, largest first, share an element, where
+// the second begins `delta` elements after the first?  They do if delta = sum of
+// d_k s_k for differences d_k of their indices.
+bool meet(int64_t delta, const Axis* x, int n) {
+  if (n == 0) return delta == 0;
+  int64_t lo = 0, hi = 0;                             // what the other axes can make up
+  for (int k = 1; k < n; ++k) {
+    lo -= (x[k].n_b - 1) * x[k].s_a;
+    hi += (x[k].n_a - 1) * x[k].s_a;
+  }
+  const int64_t s = x[0].s_a;
+  auto down = [s](int64_t v) { return v >= 0 ? v / s : -((-v + s - 1) / s); };
+  const int64_t first = std::max(-(x[0].n_b - 1), -down(hi - delta)), last = std::min(x[0].n_a - 1, down(delta - lo));
+  if (last - first > 8) return true;                  // (strides that do not nest: taken to overlap)
+  for (int64_t d = first; d <= last; ++d)
+    if (meet(delta - d * s, x + 1, n - 1)) return true;
+  return false;
+}
+
+// Do two arrays of elements of `size` bytes overlap?  Exact where their strides are
+// the same (the halves of one buffer do not), else by their first and last bytes.
+bool overlap(const void* a, const void* b, int64_t size, std::initializer_list<Axis> axes) {
+  const int64_t delta = static_cast<const char*>(b) - static_cast<const char*>(a);
+  Axis x[4];
+  int n = 0;
+  int64_t end_a = 1, end_b = 1;
+  bool exact = delta % size == 0;
+  for (Axis y : axes) {
+    end_a += (y.n_a - 1) * y.s_a;
+    end_b += (y.n_b - 1) * y.s_b;
+    if (y.n_a == 1) y.s_a = y.s_b;
+    if (y.n_b == 1) y.s_b = y.s_a;
+    if (y.s_a != y.s_b) exact = false;
+    if ((y.n_a > 1 || y.n_b > 1) && y.s_a != 0) x[n++] = y;
+  }
+  if (delta >= end_a * size || -delta >= end_b * size) return false;
+  if (!exact) return true;
+  std::sort(x, x + n, [](const Axis& l, const Axis& r) { return l.s_a > r.s_a; });
+  return meet(delta / size, x, n);
 }
 bool overlap(const TensorDesc& a, const TensorDesc& b) {
-  uintptr_t al, ah, bl, bh;
-  extent(a, &al, &ah);
-  extent(b, &bl, &bh);
-  return al < bh && bl < ah;
+  return overlap(a.ptr, b.ptr, 2,
+                 {{a.B, b.B, a.sB, b.sB}, {a.H, b.H, a.sH, b.sH}, {a.N, b.N, a.sN, b.sN}, {a.D, b.D, 1, 1}});
 }
 
 // Rows of fp32, `stride` elements apart.
 bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* b, int64_t b_stride, int64_t b_len,
                   int64_t rows) {
-  return a < b + (rows - 1) * b_stride + b_len && b < a + (rows - 1) * a_stride + a_len;
+  return overlap(a, b, 4, {{rows, rows, a_stride, b_stride}, {a_len, b_len, 1, 1}});
 }
 
 int attn(const pbs_tensor* Qt, const pbs_tensor* Kpt, const pbs_tensor* Vpt, bool prefix, const pbs_tensor* Kt,

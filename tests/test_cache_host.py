@@ -182,6 +182,26 @@ def test_evict_refusals(lib):
         assert call(**kw) == code, kw
 
 
+def test_overlapping_views_are_refused(lib):
+    """Arrays of equal strides that lie in one another and share an element."""
+    def evict(ko, vo, k=None, out=0x5000, s=256, s_out=64):
+        return lib.pbs_evict(P(0x2000), s, k or _desc(ptr=0x1000000), _desc(ptr=0x2000000), None, 64, 8, 4, P(0x3000),
+                             None, ko, vo, P(out), s_out, P(0x4000), 1 << 40, None)
+
+    ko = _desc(N=64, ptr=0x3000000)
+    row, head = 2 * 128, 2 * 64 * 128                       # bytes
+    wide = dict(N=64, sH=2 * 64 * 128, sB=4 * 64 * 128)     # heads of K_out and V_out in turn
+    for ko, vo in ((ko, _desc(N=64, ptr=0x3000000 + head)), (ko, _desc(N=64, ptr=0x3000000 - head)),
+                   (_desc(ptr=0x3000000, **wide), _desc(ptr=0x3000000 + head - row, **wide)),
+                   (_desc(ptr=0x3000000, **wide), _desc(ptr=0x3000000 - head + 16, **wide)),
+                   (_desc(N=64, ptr=0x3000000, sN=256, sH=64 * 256),                  # elements in turn
+                    _desc(N=64, ptr=0x3000000 + 2 * 128 - 16, sN=256, sH=64 * 256))):
+        assert evict(ko, vo) == -1 and b"overlap" in lib.pbs_get_last_error()
+    ko, vo = _desc(N=64, ptr=0x3000000), _desc(N=64, ptr=0x4000000)
+    for off, s in ((255, 256), (256, 319), (-63, 320), (-1, 256)):                    # behind and before mass's rows
+        assert evict(ko, vo, out=0x2000 + 4 * off, s=s, s_out=s) == -1 and b"overlap" in lib.pbs_get_last_error()
+
+
 def test_binding_refusals(lib):
     x = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)
     for call in (lambda: pbs.pbs_attn_window(x, x, x), lambda: pbs.pbs_attn_prefix(x, x, x, x, x),

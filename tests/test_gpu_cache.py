@@ -431,6 +431,31 @@ def test_evict_into_larger_buffers():
         assert (K2[b, :, n:] == 9).all() and (V2[b, :, n:] == 9).all() and (m2[b, :, n:] == 9).all()
 
 
+def test_views_of_one_buffer():
+    """Inputs and outputs that lie between one another in a buffer, sharing no
+    element, are taken: K beside V per sequence, heads or elements in turn, and
+    the short cache behind the long one."""
+    B, Hkv, d, N, budget = 3, 2, 64, 300, 70
+    Q, K, V = inputs(5, B, 4, Hkv, d, 1, N)
+    mass = torch.rand((B, Hkv, N), device="cuda")
+    want = pbs.pbs_evict(mass, K, V, budget, 10, 4)
+    room = torch.zeros((B, 2, Hkv, N + budget, d), dtype=torch.bfloat16, device="cuda")     # K beside V
+    turns = torch.zeros((B, N + budget, Hkv, 2, d), dtype=torch.bfloat16, device="cuda").permute(0, 3, 2, 1, 4)
+    side = torch.zeros((B, Hkv, N + budget, 2, d), dtype=torch.bfloat16, device="cuda").permute(0, 3, 1, 2, 4)
+    for buf in (room, turns, side):
+        m = torch.zeros((B, Hkv, N + budget), device="cuda")
+        buf[:, 0, :, :N], buf[:, 1, :, :N], m[..., :N] = K, V, mass
+        got = pbs.pbs_evict(m[..., :N], buf[:, 0, :, :N], buf[:, 1, :, :N], budget, 10, 4, K_out=buf[:, 0, :, N:],
+                            V_out=buf[:, 1, :, N:], mass_out=m[..., N:])
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert torch.equal(buf[:, 0, :, :N], K) and torch.equal(buf[:, 1, :, :N], V)
+    _, lse = pbs.pbs_attn_window(Q, K, V)
+    pair = torch.zeros((B, Hkv, 2, N), device="cuda")
+    pair[:, :, 0] = mass
+    pbs.pbs_key_mass(Q, K, lse, pair[:, :, 0], 0.5, out=pair[:, :, 1])
+    assert torch.equal(pair[:, :, 1], pbs.pbs_key_mass(Q, K, lse, mass, 0.5)) and torch.equal(pair[:, :, 0], mass)
+
+
 # ---------------------------------------------------- as a program uses them
 def test_prefill_mass_evict_decode():
     """Prefill by the sparse attention, mass of every key from its LSE, a cache
