@@ -13,9 +13,9 @@
 // Masses share their leading digits, so lanes meet on the same bin: there are four
 // copies of the histogram, by lane.
 // Bound: instructions, about 0.4 us per 1024 keys and CTA behind a fixed 7 us (three
-// digits of a few barriers each).  Measured: 128 rows of 16384 to 32768 keys 23 us.
+// digits of a few barriers each).  Measured: 128 rows of 16384 to 32768 keys 22 us.
 // The gather copies the kept rows of K and V, bound by HBM: 2 x 4 D bytes a row.
-// Measured: 128 x 4097 rows of D = 128 91 us, 5.9 TB/s.
+// Measured: 128 x 4097 rows of D = 128 84 us, 6.3 TB/s.
 #include <math.h>
 
 #include <algorithm>
@@ -243,9 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   if (n_rank > 1) cluster_sync_all();               // the others may still read this CTA's shared memory
 }
 
-// Kept rows in 16-byte chunks, four rows per thread with all their loads in
-// flight before the first store.
-constexpr int kGatherRows = 4;
+// Kept rows in 16-byte chunks, two rows of K and V per thread with all their loads in
+// flight before the first store.  Rows are read and written once: the streaming hints
+// on both sides take 128 rows of 4097 keys (D 128) from 88 to 84 us (one
+// side alone gains nothing; four rows per thread 85, eight without the hints 118).
+constexpr int kGatherRows = 2;
 template <int D>
 __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p) {
   constexpr int CH = D / 8, RP = 256 / CH;          // chunks a row, rows a pass of the CTA
@@ -268,15 +270,15 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p) 
 #pragma unroll
   for (int q = 0; q < kGatherRows; ++q) {
     if (j[q] < 0) continue;
-    x[q] = *reinterpret_cast<const uint4*>(k + j[q] * p.K.sN);
-    y[q] = *reinterpret_cast<const uint4*>(v + j[q] * p.V.sN);
+    x[q] = __ldcs(reinterpret_cast<const uint4*>(k + j[q] * p.K.sN));
+    y[q] = __ldcs(reinterpret_cast<const uint4*>(v + j[q] * p.V.sN));
   }
 #pragma unroll
   for (int q = 0; q < kGatherRows; ++q) {
     if (j[q] < 0) continue;
     const int64_t i = i0 + q * RP;
-    *reinterpret_cast<uint4*>(ko + i * p.Ko.sN) = x[q];
-    *reinterpret_cast<uint4*>(vo + i * p.Vo.sN) = y[q];
+    __stcs(reinterpret_cast<uint4*>(ko + i * p.Ko.sN), x[q]);
+    __stcs(reinterpret_cast<uint4*>(vo + i * p.Vo.sN), y[q]);
     if (c == 0) p.mass_out[row * p.mass_out_stride + i] = p.mass[row * p.mass_stride + j[q]];
   }
 }
