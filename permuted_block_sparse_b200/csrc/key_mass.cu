@@ -757,10 +757,13 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
   const int64_t G = p.Q.H / p.K.H, rows = p.Q.N * G, BH = p.K.B * p.K.H;
   if (rows <= kFewRows) {
     const int64_t rounds = (p.K.N + kWarps * kGroup - 1) / (kWarps * kGroup);
-    // One CTA for every place on the chip, with two rounds of keys at least: 8
-    // KV-head rows of 4096 keys take 4.0 us in 32 parts (6.0 in 8), 32 rows of
-    // 8192 11.3 us in 16 (21.5 in 128).
-    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds / 2, (kFewCtas * kSMs + BH - 1) / BH)));
+    // One CTA for every place on the chip and no more, with two rounds of keys at
+    // least; 16 rounds a CTA where that makes more of them, so that sequences of
+    // unequal length even out.  8 KV-head rows of 4096 keys take 4.0 us in 32 parts
+    // (6.0 in 8); 64 rows of up to 8192 20.4 us in 9 (23.0 in 10, which take a second
+    // round); 256 rows 67 us in 8 (73 in 3), of 2048 36 us in 2 (38 in 5).
+    const int64_t want = std::max(kFewCtas * kSMs / BH, rounds / 16);
+    const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds / 2, want)));
     const int bytes = kWarps * kStages * kGroup * D * 2;
     static std::atomic<uint64_t> done[2];
     auto kernel = rows <= 8 ? mass_few_kernel<D, 1> : mass_few_kernel<D, 2>;
