@@ -31,10 +31,11 @@ __device__ __forceinline__ void write_mass(const KeyMassParams& p, int64_t bh, i
 // Up to 16 query rows per KV head (a decode step).  Four warps per CTA; each
 // warp streams groups of 16 keys through a private cp.async ring and multiplies
 // them as the A operand of m16n8k16 (keys x rows); the queries stay in registers
-// as the B operand.  A CTA's rounds of 64 keys are spread over the cache, so
-// that the keys outside a window, which are not loaded, fall on all CTAs alike.
+// as the B operand.  Groups that no row sees (outside a window) are not among them:
+// their mass is carried over beside the first loads.  The CTAs take groups in turn.
 // Bound: HBM, 2 D bytes per visible key.  Measured: 32 sequences of 4096 to 8192 keys
-// (Hq 32, Hkv 8, D 128) 72 us, 5.9 TB/s.
+// (Hq 32, Hkv 8, D 128) 66 us, 6.4 TB/s; 200 rows of 30000 keys under a window of 1000
+// 33 us (88 with the unseen groups in the loop).
 // Sixteen warps per SM (four CTAs of 48 KB) hide the chain from a group's arrival
 // to its sums; with eight the schedulers issued in 41% of the cycles.
 constexpr int kWarps = 4;
@@ -59,6 +60,13 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
   const int lo_min = max(0, first - window + 1);
   const int lo_max = max(0, L - window);
   const int seen_end = nq > 0 ? L : 0;
+  // groups of 16 keys that hold one of them: below g_sink, and g_low to g_end
+  const int g_sink = (min(n_sink, seen_end) + kGroup - 1) / kGroup;
+  const int g_end = max(g_sink, (seen_end + kGroup - 1) / kGroup), g_low = min(g_end, max(g_sink, lo_min / kGroup));
+  const int n_group = g_sink + g_end - g_low, gap_groups = g_low - g_sink;
+  constexpr int kNone = 0x7fffff00;               // past every key
+  // first key of the v-th of them
+  auto key_of = [&](int v) { return v < n_group ? (v + (v < g_sink ? 0 : gap_groups)) * kGroup : kNone; };
 
   uint32_t qb[NG][D / 16][2];                     // Q as B fragments: row lane / 4 of each eight
   float y[NG][2];                                 // and the lse of rows 2 (lane mod 4) + {0, 1}
@@ -94,10 +102,9 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
   // this lane's chunk of its rows of group 0, and from there to its next row
   const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + hk * p.K.sH + lc * 8;
   const int64_t sN = p.K.sN;
-  const int stride = n_parts * kWarps * kGroup;
-  auto some = [&](int j0) { return j0 < seen_end && (j0 + kGroup > lo_min || j0 < n_sink); };
+  const int stride = n_parts * kWarps;
   auto load = [&](int j0, int st) {
-    if (some(j0)) {
+    if (j0 < seen_end) {
       const uint32_t dst = ring + st * kTile;
       if (j0 + kGroup <= L && (j0 >= lo_min || j0 + kGroup <= n_sink)) {
         const __nv_bfloat16* src = kb + (j0 + lr) * sN;
@@ -120,52 +127,72 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
   const float* prev = p.prev && (lane & 3) < 2 ? p.prev + bh * p.prev_stride + mine : nullptr;
   float* mass = p.mass + bh * p.mass_stride + mine;
   auto earlier = [&](int j0) { return prev && j0 + mine < L ? prev[j0] : 0.f; };
-  int j0 = (part * kWarps + warp) * kGroup;
+  // this warp's group, the next and the one after
+  int v = part * kWarps + warp, j0 = key_of(v), j1 = key_of(v + stride), j2;
+  static_assert(kStages == 3, "two groups ahead");
+  load(j0, 0);
+  load(j1, 1);
+  // keys of the other groups, which no row sees, while those land
+  {
+    const float* old = p.prev ? p.prev + bh * p.prev_stride : nullptr;
+    float* out = p.mass + bh * p.mass_stride;
+    const int gap = gap_groups * kGroup, n = gap + max(0, N - g_end * kGroup);
+    auto at = [&](int i) { return i < gap ? g_sink * kGroup + i : g_end * kGroup + i - gap; };
+    constexpr int kAhead = 4, kStep = kWarps * 32;
+    for (int i = part * kAhead * kStep + tid; i < n; i += n_parts * kAhead * kStep) {
+      float x[kAhead];
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load(j0 + i * stride, i);
+      for (int e = 0; e < kAhead; ++e) {
+        const int j = at(i + e * kStep);
+        x[e] = old && i + e * kStep < n && j < L ? p.decay * old[j] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (i + e * kStep < n) out[at(i + e * kStep)] = x[e];
+    }
+  }
   int st = 0;
   float next_old = earlier(j0);
-  for (; j0 < N; j0 += stride) {
+  for (; j0 < seen_end; j0 = j1, j1 = j2, v += stride) {
+    j2 = key_of(v + 2 * stride);
     const float old = next_old;
-    next_old = earlier(j0 + stride);
+    next_old = earlier(j1);
     cp_async_wait<kStages - 2>();
     __syncwarp();
-    load(j0 + (kStages - 1) * stride, st == 0 ? kStages - 1 : st - 1);
+    load(j2, st == 0 ? kStages - 1 : st - 1);
     const uint32_t sk = ring + st * kTile;
     st = st == kStages - 1 ? 0 : st + 1;
     float sum[2] = {0.f, 0.f};                    // keys lane / 4 and 8 + lane / 4
-    if (some(j0)) {
-      float s[NG][4];
+    float s[NG][4];
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[g][e] = 0.f;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        // matrices: keys 0-7 | 8-15 | 0-7 | 8-15, chunks 2k | 2k | 2k+1 | 2k+1
-        uint32_t f[4];
-        ldsm4(f, sk + rows_offset<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * k + (lane >> 4)));
+    for (int k = 0; k < D / 16; ++k) {
+      // matrices: keys 0-7 | 8-15 | 0-7 | 8-15, chunks 2k | 2k | 2k+1 | 2k+1
+      uint32_t f[4];
+      ldsm4(f, sk + rows_offset<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * k + (lane >> 4)));
 #pragma unroll
-        for (int g = 0; g < NG; ++g) mma_16816(s[g], f[0], f[1], f[2], f[3], qb[g][k][0], qb[g][k][1]);
-      }
-      const bool full = j0 + kGroup - 1 <= first && (j0 >= lo_max || j0 + kGroup <= n_sink);
+      for (int g = 0; g < NG; ++g) mma_16816(s[g], f[0], f[1], f[2], f[3], qb[g][k][0], qb[g][k][1]);
+    }
+    const bool full = j0 + kGroup - 1 <= first && (j0 >= lo_max || j0 + kGroup <= n_sink);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+    for (int g = 0; g < NG; ++g) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float w = ex2(fmaf(s[g][e], p.scale_log2, -y[g][e & 1]));
-          if (!full) {
-            const int j = j0 + (e >> 1) * 8 + lane / 4, at = pos[g][e & 1];
-            if (j > at || (j <= at - window && j >= n_sink)) w = 0.f;
-          }
-          sum[e >> 1] += w;
+      for (int e = 0; e < 4; ++e) {
+        float w = ex2(fmaf(s[g][e], p.scale_log2, -y[g][e & 1]));
+        if (!full) {
+          const int j = j0 + (e >> 1) * 8 + lane / 4, at = pos[g][e & 1];
+          if (j > at || (j <= at - window && j >= n_sink)) w = 0.f;
         }
+        sum[e >> 1] += w;
       }
+    }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-        sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-      }
+    for (int e = 0; e < 2; ++e) {
+      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
     }
     if ((lane & 3) < 2 && j0 + mine < N)
       mass[j0] = j0 + mine < L ? fmaf(p.decay, old, (lane & 3) ? sum[1] : sum[0]) : 0.f;
@@ -758,11 +785,12 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
   if (rows <= kFewRows) {
     const int64_t rounds = (p.K.N + kWarps * kGroup - 1) / (kWarps * kGroup);
     // One CTA for every place on the chip and no more, with two rounds of keys at
-    // least; 16 rounds a CTA where that makes more of them, so that sequences of
+    // least; 16 rounds of visible keys a CTA where that makes more of them, so that sequences of
     // unequal length even out.  8 KV-head rows of 4096 keys take 4.0 us in 32 parts
     // (6.0 in 8); 64 rows of up to 8192 20.4 us in 9 (23.0 in 10, which take a second
-    // round); 256 rows 67 us in 8 (73 in 3), of 2048 36 us in 2 (38 in 5).
-    const int64_t want = std::max(kFewCtas * kSMs / BH, rounds / 16);
+    // round); 256 rows 66 us in 8 (73 in 3), of 2048 36 us in 2 (38 in 5).
+    const int64_t seen = std::min(rounds, (p.mask.window + p.mask.n_sink + p.Q.N) / (kWarps * kGroup) + 2);
+    const int64_t want = std::max(kFewCtas * kSMs / BH, seen / 16);
     const int parts = static_cast<int>(std::max<int64_t>(1, std::min(rounds / 2, want)));
     const int bytes = kWarps * kStages * kGroup * D * 2;
     static std::atomic<uint64_t> done[2];

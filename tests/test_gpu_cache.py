@@ -305,6 +305,10 @@ MASS_CASES = [
     (1, 3, 1, 64, 90, 50, 0, 0, None, None),                         # more rows than keys
     (1, 8, 1, 128, 600, 5000, 0, 0, None, None),                     # parts of the rows
     (300, 2, 2, 64, 1, 70, 20, 2, None, None),
+    (4, 2, 2, 64, 1, 4099, 17, 33, [4099, 66, 34, 1], None),         # sinks, a gap, the window, the unfilled end
+    (5, 4, 1, 128, 2, 2000, 1, 0, [2000, 17, 16, 15, 0], [2, 1, 2, 0, 2]),
+    (3, 3, 3, 64, 9, 700, 5, 16, [700, 40, 9], [9, 3, 9]),
+    (2, 2, 1, 128, 1, 65, 1, 65, [65, 64], None),
     (40, 8, 4, 64, 200, 300, 0, 0, None, None),                      # several launches, each adding to the last
     (75, 8, 2, 128, 150, 200, 70, 9, [200, 0, 150, 31, 199] * 15, [150, 0, 64, 65, 128] * 15),
     (1, 8, 4, 128, 512, 9500, 3000, 5, None, None),
