@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
       if (j0 + kGroup <= L && (j0 >= lo_min || j0 + kGroup <= n_sink)) {
         const __nv_bfloat16* src = kb + (j0 + lr) * sN;
 #pragma unroll
-        for (int it = 0; it < kGroup / RPI; ++it, src += RPI * sN) cp_async16(dst + rows_offset<D>(it * RPI + lr, lc), src);
+        for (int it = 0; it < kGroup / RPI; ++it, src += RPI * sN)
+          cp_async16(dst + rows_offset<D>(it * RPI + lr, lc), src);
       } else {
 #pragma unroll
         for (int it = 0; it < kGroup / RPI; ++it) {
@@ -508,8 +509,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
 }
 
 // ---------------------------------------------------------- some hundred rows
-// 256 query rows per KV head (drafted tokens, the last rows of a prompt) and, in up to
-// four launches that each add to the one before, 1024 over many keys.  The other way
+// Up to 256 query rows per KV head (drafted tokens, the last rows of a prompt); in up to
+// four launches, each adding to the one before, 1024 over many keys.  The other way
 // round: the queries (one or two boxes) and their lse stay in shared memory and the
 // key tiles stream past, through a ring of four, in pairs that two groups of eight
 // consumer warps take.  Each group has two tensor-memory buffers.  CTAs are one per
