@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libpbs.so")
 SOURCES = ["api.cu", "permute.cu", "permute_seg.cu", "select.cu", "select_sample.cu", "attn_fwd.cu",
            "attn_fwd_pair.cu", "permute_queries.cu",
            "permute_noalloc.cu", "cache_api.cu", "cache_attn.cu", "cache_attn_wide.cu", "key_mass.cu", "evict.cu"]
-HEADERS = ["pbs_common.cuh", "pbs_internal.h", "cache_common.cuh", "cache_attn.cuh", "mma_sync.cuh"]
+HEADERS = ["pbs_common.cuh", "pbs_internal.h", "cache_common.cuh", "cache_attn.cuh", "mma_sync.cuh", "wide_order.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 

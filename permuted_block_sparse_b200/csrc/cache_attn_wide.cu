@@ -46,6 +46,7 @@
 #include <algorithm>
 
 #include "cache_attn.cuh"
+#include "wide_order.h"
 
 namespace pbs {
 
@@ -183,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     lo_last1 = run.lo(last_pos(1), p.mask.window);
   }
   auto active = [&](int h, int t) {
-    const int up = h ? hi_last1 : hi_last0, low = h ? lo_first1 : lo_first0;
-    return h < n_slot && 128 * t <= up && (128 * t + 127 >= low || 128 * t < run.n_sink);
+    return h < n_slot && slot_uses(t, h ? hi_last1 : hi_last0, h ? lo_first1 : lo_first0, run.n_sink);
   };
   auto full = [&](int h, int t) {
     const int up = h ? hi_first1 : hi_first0, low = h ? lo_last1 : lo_last0;
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
     auto landed = [&](uint64_t* bars, int& seen, int t) {
       for (; ok && seen <= t; ++seen) wait(&bars[(seen - t0) % NS], ((seen - t0) / NS) & 1);
     };
-    auto last_user = [&](int h, int t) { return h == 1 || !active(1, t); };
     int done0 = 0, done1 = 0;               // tiles whose QK^T has been issued, per slot
+    int on0 = t0 - 1, on1 = t0 - 1;         // and the last of them
     auto qk = [&](int h, int t) {
       landed(sh.bar_k, k_seen, t);
       if (!ok) return;
@@ -333,15 +333,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
       }
       if (elect_one()) {
         tc_commit(&sh.bar_s[h]);
-        if (last_user(h, t)) tc_commit(&sh.bar_kempty[st]);
+        if (k_free(t, active(h ^ 1, t), h ? on0 : on1)) tc_commit(&sh.bar_kempty[st]);
       }
       __syncwarp();
       ++(h ? done1 : done0);
+      (h ? on1 : on0) = t;
     };
     auto next = [&](int h, int t) {
       while (t < t1 && !active(h, t)) ++t;
       return t;
     };
+    // (a host test replays this order)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = next(h, t0);
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const CacheAttnP
             mma_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, sdesc_add(b0, kk * 2048), idesc_pv,
                    kk > 0 || o_init[h] ? 1u : 0u);
         o_init[h] = true;
-        if (last_user(h, t) && elect_one()) tc_commit(&sh.bar_vempty[st]);
+        if (v_free(h, active(h ^ 1, t)) && elect_one()) tc_commit(&sh.bar_vempty[st]);
         __syncwarp();
         const int tn = next(h, t + 1);
         if (tn < t1) qk(h, tn);
