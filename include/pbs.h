@@ -90,7 +90,8 @@ enum { PBS_SELECT_SCORE_ORDER = 0x10, PBS_SELECT_PERM_PER_SEGMENT = 0x20 };
 /* pbs_attn_fwd_ex flags. */
 enum { PBS_ATTN_EARLY_STOP = 1, PBS_ATTN_PERM_PER_SEGMENT = 2, PBS_ATTN_CTA_PAIR = 4 };
 
-/* Bytes of workspace the given op needs for these shapes (0 if none).
+/* Bytes of workspace the given op needs for these shapes (0 if none, or for
+ * a cache operator where it refuses the shapes).
  * Q and K may not be NULL; only their shapes are read.  The cache
  * operators (PBS_OP_ATTN_WINDOW and after) do not read blk and seg; for
  * PBS_OP_ATTN_PREFIX K is the sequences' own cache, and for PBS_OP_EVICT Q

@@ -232,8 +232,10 @@ size_t pbs_workspace_size(int op, const pbs_tensor* Qt, const pbs_tensor* Kt, in
   switch (op) {
     case PBS_OP_ATTN_WINDOW:
     case PBS_OP_ATTN_PREFIX:
+      if (pbs::api_check_cache_shapes(Q, K)) return 0;
       return align256(pbs::cache_attn_ws_bytes(Q, K, op == PBS_OP_ATTN_PREFIX));
     case PBS_OP_KEY_MASS:
+      if (pbs::api_check_cache_shapes(Q, K)) return 0;
       return align256(pbs::key_mass_ws_bytes(Q, K));
     case PBS_OP_EVICT:
       return align256(pbs::evict_ws_bytes(K));

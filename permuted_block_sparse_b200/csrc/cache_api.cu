@@ -34,13 +34,7 @@ bool broadcast(const TensorDesc& t) { return (t.H > 1 && t.sH == 0) || (t.B > 1 
 
 // Queries against a cache: shapes, head groups and the mask's numbers.
 int check_pair(const TensorDesc& Q, const TensorDesc& K, int64_t window, int n_sink, float scale) {
-  if (Q.B != K.B || Q.D != K.D) return fail(PBS_ERR_INVALID_ARG, "Q and K disagree on B or D");
-  if (Q.H % K.H)
-    return fail(PBS_ERR_INVALID_ARG, "Hq %lld not a multiple of Hkv %lld", (long long)Q.H, (long long)K.H);
-  if (Q.H / K.H > 64) return fail(PBS_ERR_UNSUPPORTED, "Hq / Hkv %lld > 64", (long long)(Q.H / K.H));
-  if (Q.B > 65535 || K.H > 65535 || Q.B * K.H > 65535)
-    return fail(PBS_ERR_UNSUPPORTED, "B * Hkv above 65535");
-  if (Q.B * Q.H * Q.N >= (1ll << 31)) return fail(PBS_ERR_UNSUPPORTED, "B * Hq * M above 2^31");
+  if (const int rc = pbs::api_check_cache_shapes(Q, K)) return rc;
   if (broadcast(Q)) return fail(PBS_ERR_UNSUPPORTED, "Q may not be a broadcast view (zero head or batch stride)");
   if (window < 0 || n_sink < 0) return fail(PBS_ERR_INVALID_ARG, "window/n_sink negative");
   if (!(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f))
@@ -150,6 +144,23 @@ int attn(const pbs_tensor* Qt, const pbs_tensor* Kpt, const pbs_tensor* Vpt, boo
 }
 
 }  // namespace
+
+namespace pbs {
+
+// (the plans of the kernels divide by the rows that fit a tile: they are only made for
+// shapes that pass)
+int api_check_cache_shapes(const TensorDesc& Q, const TensorDesc& K) {
+  if (Q.B != K.B || Q.D != K.D) return fail(PBS_ERR_INVALID_ARG, "Q and K disagree on B or D");
+  if (Q.H % K.H)
+    return fail(PBS_ERR_INVALID_ARG, "Hq %lld not a multiple of Hkv %lld", (long long)Q.H, (long long)K.H);
+  if (Q.H / K.H > 64) return fail(PBS_ERR_UNSUPPORTED, "Hq / Hkv %lld > 64", (long long)(Q.H / K.H));
+  if (Q.B > 65535 || K.H > 65535 || Q.B * K.H > 65535)
+    return fail(PBS_ERR_UNSUPPORTED, "B * Hkv above 65535");
+  if (Q.B * Q.H * Q.N >= (1ll << 31)) return fail(PBS_ERR_UNSUPPORTED, "B * Hq * M above 2^31");
+  return PBS_OK;
+}
+
+}  // namespace pbs
 
 extern "C" {
 

@@ -520,7 +520,6 @@ Plan plan(const TensorDesc& Q, const TensorDesc& K, int64_t keys, bool has_prefi
 }  // namespace
 
 size_t cache_attn_ws_bytes(const TensorDesc& Q, const TensorDesc& K, bool prefix) {
-  if (Q.H % K.H || K.H > Q.H) return 0;
   // a window only makes for fewer parts; the prefix's length is not known here
   const Plan w = plan(Q, K, K.N, prefix, 1ll << 31);
   const int64_t n = w.own + w.prefix;

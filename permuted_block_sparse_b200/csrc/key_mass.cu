@@ -838,7 +838,6 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t s) {
 }  // namespace
 
 size_t key_mass_ws_bytes(const TensorDesc& Q, const TensorDesc& K) {
-  if (K.H > Q.H || Q.H % K.H) return 0;
   const int parts = mass_parts(Q, K);
   return parts == 1 ? 0 : static_cast<size_t>(parts) * K.B * K.H * K.N * sizeof(double);
 }

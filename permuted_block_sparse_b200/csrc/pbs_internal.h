@@ -63,6 +63,7 @@ int api_ok();
 int* api_device_error_word();
 int api_check_tensor(const pbs_tensor* t, const char* name, TensorDesc* out);
 int api_check_ws(void* ws, size_t ws_bytes, size_t need);
+int api_check_cache_shapes(const TensorDesc& Q, const TensorDesc& K);
 int api_validate_permute(const pbs_tensor* Qt, const pbs_tensor* Kt, int blk, int seg, int n_sink,
                          const int32_t* perm, TensorDesc* Q, TensorDesc* K);
 

@@ -1,5 +1,4 @@
-"""Cache operators on the GPU at edges of their kernels: slots whose windows start
-on tile bounds."""
+"""Cache operators on the GPU at edges of their kernels and at their limits."""
 import pytest
 import torch
 
@@ -24,3 +23,13 @@ def test_one_head_per_kv_head_windows_on_tile_bounds(M, N, window, n_sink, d):
             one = [t[:, h:h + 1] for t in (Q, K, V)]
             cu.assert_attention(O[:, h:h + 1], lse[:, h:h + 1], cu.reference(*one, window, n_sink),
                                 torch.ones(1, M, dtype=torch.bool, device="cuda"), f"seed {seed}, head {h}")
+
+
+def test_head_groups_past_the_limit_are_refused():
+    Q, K, V = inputs(1, 1, 129, 1, 64, 4, 300)
+    lse = torch.zeros((1, 129, 4), device="cuda")
+    for call in (lambda: pbs.pbs_attn_window(Q, K, V), lambda: pbs.pbs_attn_prefix(Q, K, V, K, V),
+                 lambda: pbs.pbs_key_mass(Q, K, lse)):
+        with pytest.raises(pbs.PbsError) as e:
+            call()
+        assert e.value.code == -2
