@@ -27,6 +27,33 @@ __device__ __forceinline__ void write_mass(const KeyMassParams& p, int64_t bh, i
   p.mass[bh * p.mass_stride + j] = x;
 }
 
+// Sums 2^(scale s - y) over 32 columns of a product (`v`, one key a thread) into a2, the
+// whole of it or the columns in `see`.  A column that is left out is taken out of the
+// finished exponent: its own s or y may be NaN.
+template <bool WHOLE>
+__device__ __forceinline__ void add_weights(const uint32_t (&v)[32], const float* ny, unsigned long long sc2,
+                                            uint32_t see, unsigned long long (&a2)[4]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(ny + e);
+    float t[4];
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, n2.x), t[0], t[1]);
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, n2.y), t[2], t[3]);
+    if (!WHOLE) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (!(see & (1u << (e + q)))) t[q] = -INFINITY;
+    }
+    a2[(e / 2) & 3] = f2_add(a2[(e / 2) & 3], f2_pack(ex2(t[0]), ex2(t[1])));
+    a2[(e / 2 + 1) & 3] = f2_add(a2[(e / 2 + 1) & 3], f2_pack(ex2(t[2]), ex2(t[3])));
+  }
+}
+// Bits of the columns c .. c + 31 that lie in c_lo .. c_hi - 1.
+__device__ __forceinline__ uint32_t columns_in(int c, int c_lo, int c_hi) {
+  const int lo = c_lo - c, up = c_hi - c;
+  return (up <= 0 ? 0u : up >= 32 ? ~0u : (1u << up) - 1u) & ~(lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1u);
+}
+
 // ------------------------------------------------------------------ few rows
 // Up to 16 query rows per KV head (a decode step).  Four warps per CTA; each
 // warp streams groups of 16 keys through a private cp.async ring and multiplies
@@ -85,7 +112,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int c = g * 8 + (lane & 3) * 2 + e;
-      y[g][e] = INFINITY;                         // no query: weight 0
+      y[g][e] = INFINITY;                         // no query
       pos[g][e] = -1;
       if (c < nq * G) {
         const float x = p.lse[(static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + c / G];
@@ -183,8 +210,10 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float w = ex2(fmaf(s[g][e], p.scale_log2, -y[g][e & 1]));
+        const int at = pos[g][e & 1];
+        if (at < 0) w = 0.f;                      // (a NaN or infinity of the key makes w NaN without a query too)
         if (!full) {
-          const int j = j0 + (e >> 1) * 8 + lane / 4, at = pos[g][e & 1];
+          const int j = j0 + (e >> 1) * 8 + lane / 4;
           if (j > at || (j <= at - window && j >= n_sink)) w = 0.f;
         }
         sum[e >> 1] += w;
@@ -242,6 +271,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
   __shared__ uint32_t tmem_base;
   __shared__ int abort_sh;
   __shared__ __align__(16) float ny[NS][128];         // -log2(e) lse of the box's rows
+  __shared__ uint2 live[NS][2];                       // bits of the rows that add something (lse not -inf)
   __shared__ double half_sum[256];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_previous_kernel();
@@ -338,8 +368,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
     auto lse_of = [&](int x, float (&v)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float l = x < x1 && x * pm + in_box[e] < n_left ? lse[e][x * pm] : -INFINITY;
-        v[e] = l == -INFINITY ? -INFINITY : -l * kLog2e;    // -inf: the row adds nothing
+        v[e] = x < x1 && x * pm + in_box[e] < n_left ? lse[e][x * pm] : -INFINITY;    // -inf: the row adds nothing
       }
     };
     float v[NS][4], ahead[NS][4];
@@ -362,7 +391,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
           if (ok = __all_sync(0xffffffffu, ok); !ok) break;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ny[s][lane + 32 * e] = v[s][e];
+        for (int e = 0; e < 4; ++e) {
+          ny[s][lane + 32 * e] = -v[s][e] * kLog2e;
+          const uint32_t some = __ballot_sync(0xffffffffu, v[s][e] != -INFINITY);
+          if (lane == e) reinterpret_cast<uint32_t*>(live[s])[e] = some;
+        }
         mbar_arrive(&bar_y[s]);
       }
 #pragma unroll
@@ -454,30 +487,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_wide_kernel(const KeyMas
       const int ahead = static_cast<int>(j) - at;
       const int hi = j < n_sink ? nq - row : min(nq - row, ahead + window);
       const int c_lo = min(pm, max(0, ahead)) * G, c_hi = j < L ? min(pm, max(0, hi)) * G : 0;
-      const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128);
+      const uint2 some = live[s][half];
+      const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128 && (some.x & some.y) == ~0u);
       const bool none = __all_sync(0xffffffffu, c_lo >= c_hi);
       unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
       for (int c = half * 64; c < min(none ? 0 : n_mma, half * 64 + 64); c += 32) {
         uint32_t v[32];
         tmem_ld32(tS + d * 128 + (c & 32), v);
-        if (!full) {                              // (columns past the box are past c_hi)
-          const int lo = c_lo - c, up = c_hi - c;
-          const uint32_t see = (up <= 0 ? 0u : up >= 32 ? ~0u : (1u << up) - 1u) &
-                               ~(lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1u);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(see & (1u << e))) v[e] = __float_as_uint(-INFINITY);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(&ny[s][c + e]);
-          float t0, t1, t2, t3;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, n2.x), t0, t1);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, n2.y), t2, t3);
-          a2[(e / 2) & 3] = f2_add(a2[(e / 2) & 3], f2_pack(ex2(t0), ex2(t1)));
-          a2[(e / 2 + 1) & 3] = f2_add(a2[(e / 2 + 1) & 3], f2_pack(ex2(t2), ex2(t3)));
-        }
+        if (full) add_weights<true>(v, &ny[s][c], sc2, ~0u, a2);
+        else                                      // (columns past the box are past c_hi)
+          add_weights<false>(v, &ny[s][c], sc2, columns_in(c, c_lo, c_hi) & (c & 32 ? some.y : some.x), a2);
       }
       tc_fence_before();
       __syncwarp();
@@ -542,6 +562,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
   __shared__ uint32_t tmem_base;
   __shared__ int abort_sh;
   __shared__ __align__(16) float ny[2][128];          // -log2(e) lse of the boxes' rows
+  __shared__ uint2 live[2][2];                        // bits of the rows that add something (lse not -inf)
   __shared__ float group_sum[2][2][128];              // [group][parity of the pair][key]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_previous_kernel();
@@ -582,11 +603,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
         make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async();
-  if (tid < 256) {                                    // -inf: the row adds nothing
+  if (tid < 256) {
     const int c = tid & 127, r = (tid >> 7) * pm + c / G;
     const int64_t at = (static_cast<int64_t>(b) * Hq + hk * G + c % G) * M + base + r;
     const float l = c < cols && r < nq ? p.lse[at] : -INFINITY;
-    ny[tid >> 7][c] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+    ny[tid >> 7][c] = -l * kLog2e;
+    const uint32_t some = __ballot_sync(0xffffffffu, l != -INFINITY);      // (-inf: the row adds nothing)
+    if (lane == 0) reinterpret_cast<uint32_t*>(live)[warp] = some;
   }
   if (warp == 0) {
     tmem_alloc(&tmem_base, 512);
@@ -694,30 +717,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) mass_mid_kernel(const KeyMass
         const int ahead = j - at;                     // at most 128 + 256, before the window is added
         const int hi = j < n_sink ? nq - row : min(nq - row, ahead + window);
         const int c_lo = min(pm, max(0, ahead)) * G, c_hi = j < L ? min(pm, max(0, hi)) * G : 0;
-        const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128);
+        const uint2 some = live[x][half];
+        const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == 128 && (some.x & some.y) == ~0u);
         const bool none = __all_sync(0xffffffffu, c_lo >= c_hi);
         unsigned long long a2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
         for (int c = half * 64; c < min(none ? 0 : n_mma, half * 64 + 64); c += 32) {
           uint32_t v[32];
           tmem_ld32(tS + d * 128 + (c & 32), v);
-          if (!full) {                                // (columns past the box are past c_hi)
-            const int lo = c_lo - c, up = c_hi - c;
-            const uint32_t see = (up <= 0 ? 0u : up >= 32 ? ~0u : (1u << up) - 1u) &
-                                 ~(lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1u);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see & (1u << e))) v[e] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(&ny[x][c + e]);
-            float t0, t1, t2, t3;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, n2.x), t0, t1);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sc2, n2.y), t2, t3);
-            a2[(e / 2) & 3] = f2_add(a2[(e / 2) & 3], f2_pack(ex2(t0), ex2(t1)));
-            a2[(e / 2 + 1) & 3] = f2_add(a2[(e / 2 + 1) & 3], f2_pack(ex2(t2), ex2(t3)));
-          }
+          if (full) add_weights<true>(v, &ny[x][c], sc2, ~0u, a2);
+          else                                        // (columns past the box are past c_hi)
+            add_weights<false>(v, &ny[x][c], sc2, columns_in(c, c_lo, c_hi) & (c & 32 ? some.y : some.x), a2);
         }
         tc_fence_before();
         __syncwarp();
