@@ -337,7 +337,10 @@ int pbs_attn_fwd_ex(const pbs_tensor* Q, const pbs_tensor* K, const pbs_tensor* 
  *    strides); Q and O may not.  Hkv * B is at most 65535.
  *  - Outputs may not overlap inputs (but see prev of pbs_key_mass).
  *  - What a row sees decides its result: NaN or infinity in a key, or in the
- *    value of a key, that the row does not see leaves it unchanged.
+ *    value of a key, that the row does not see leaves it unchanged.  An
+ *    infinity or NaN in a value that it does see is what the column becomes
+ *    (an infinity may also become NaN where its weight is below the range of
+ *    fp32).
  *  - Two calls that may overlap in time need two workspaces, also where they
  *    are captured into graphs.                                               */
 

@@ -86,6 +86,10 @@ __device__ __forceinline__ void few_nonfinite(unsigned char* v, const FewRow* ro
   __syncwarp();
 }
 
+// hi V + lo V of a column.  Where a value is infinite or NaN, hi V is what its weight
+// times the value is; lo V is NaN or of the wrong sign, as lo is zero or negative.
+__device__ __forceinline__ float hi_and_lo(float hi, float lo) { return isfinite(hi) ? hi + lo : hi; }
+
 template <int D, int NG>
 __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAttnParams p, const AttnParts parts,
                                                                   const int prefix_ctas, const int n_rank) {
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_few_kernel(const CacheAtt
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)
         *reinterpret_cast<float2*>(so + (warp * NG * 8 + i) * D + j * 8 + (lane & 3) * 2) =
-            make_float2((o[g][j][0] + o[g][j][2]) * a, (o[g][j][1] + o[g][j][3]) * a);
+            make_float2(hi_and_lo(o[g][j][0], o[g][j][2]) * a, hi_and_lo(o[g][j][1], o[g][j][3]) * a);
     } else {
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)

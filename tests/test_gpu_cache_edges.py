@@ -93,3 +93,42 @@ def test_mass_of_keys_of_weight_zero(case):
     K[:, :, inf_at, 3] = -float("inf")
     assert (pbs.pbs_key_mass(Q, K, off, window=window, n_sink=n_sink) == 0).all()
     pbs.pbs_check_device()
+
+
+# B, Hq, Hkv, d, M, N, P: few rows (8, 16 and 32 a KV head) and tiles, with and without a prefix
+VALUE_FORMS = [(2, 4, 2, 128, 1, 900, 0), (2, 8, 2, 64, 2, 900, 0), (1, 16, 1, 128, 1, 5000, 0), (1, 16, 1, 64, 2, 900, 0),
+               (2, 8, 2, 128, 150, 900, 0), (2, 4, 2, 128, 1, 700, 600), (9, 8, 2, 64, 1, 700, 600)]
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("case", VALUE_FORMS, ids=str)
+def test_infinite_values_that_every_row_sees(case, bad):
+    """In the middle of the cache, where groups and tiles are wholly visible: with
+    weights of every rounding, the one that is exactly 1 among them."""
+    B, Hq, Hkv, d, M, N, P = case
+    Q, K, V = inputs(700 + N + M, B, Hq, Hkv, d, M, N)
+    Kp, Vp = (inputs(800 + P, 1, Hkv, Hkv, d, P, P)[1:] if P else (None, None))
+    run = (lambda K, V, Vp: pbs.pbs_attn_prefix(Q, Kp, Vp, K, V)) if P else (lambda K, V, Vp: pbs.pbs_attn_window(Q, K, V))
+    K[:, :, 400] = 3 * Q[:, ::Hq // Hkv, 0].sign()          # the largest logit of the groups' first heads
+    want, want_lse = run(K, V, Vp)
+    V2, Vp2 = V.clone(), None if Vp is None else Vp.clone()
+    at = [200 + 7 * c for c in range(d // 2)]               # column 2 c holds one at key 200 + 7 c
+    for c, j in enumerate(at):
+        V2[:, :, 400 if c == 3 else j, 2 * c] = bad
+    if P:
+        Vp2[:, :, 111, 1] = bad
+    O, lse = run(K, V2, Vp2)
+    pbs.pbs_check_device()
+    hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+    hit[::2], hit[1] = True, bool(P)
+    assert torch.equal(lse, want_lse) and torch.equal(O[..., ~hit], want[..., ~hit])
+    got = O[..., hit].float()
+    assert torch.isnan(got).all() if bad != bad else (got == bad).all()
+
+
+def test_infinite_values_of_both_signs():
+    Q, K, V = inputs(900, 1, 4, 2, 128, 1, 900)
+    V[:, :, 300, 5], V[:, :, 500, 5], V[:, :, 300, 6] = float("inf"), -float("inf"), float("inf")
+    O, _ = pbs.pbs_attn_window(Q, K, V)
+    assert torch.isnan(O[..., 5]).all() and (O[..., 6] == float("inf")).all()
+    assert torch.isfinite(O[..., :5]).all() and torch.isfinite(O[..., 7:]).all()
