@@ -395,7 +395,8 @@ int pbs_key_mass(const pbs_tensor* Q, const pbs_tensor* K, const float* lse, con
  *   budget in [1, N], n_sink + recent <= budget.
  *   keep: DEVICE int32 [B, Hkv, budget], the kept positions in ascending
  *     order, -1 after the last.
- *   new_len: DEVICE int32 [B], min(kv_len[b], budget); NULL if not wanted.
+ *   new_len: DEVICE int32 [B], min(kv_len[b], budget); may be the same buffer
+ *     as kv_len; NULL if not wanted.
  *   K_out, V_out: bf16 [B, Hkv, N_out, D] with N_out >= budget, the kept rows
  *     in that order; mass_out: DEVICE fp32, rows mass_out_stride (>= budget)
  *     elements apart, their mass.  Rows at and after new_len[b] are left as

@@ -546,7 +546,8 @@ def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int,
     every cache cut to ``budget`` keys, of which the first ``n_sink`` and the
     last ``recent`` always stay and the rest are those of highest ``mass``.
     ``K_out`` and ``V_out`` [B, Hkv, n >= budget, D] and ``mass_out``
-    [B, Hkv, n >= budget] take the kept rows at their start."""
+    [B, Hkv, n >= budget] take the kept rows at their start.  ``new_len`` may be
+    ``kv_len`` itself."""
     lib = _lib or load()
     k, v = describe(K), describe(V)
     B, Hkv, N, D = K.shape

@@ -113,6 +113,11 @@ bool rows_overlap(const float* a, int64_t a_stride, int64_t a_len, const float* 
   return overlap(a, b, 4, {{rows, rows, a_stride, b_stride}, {a_len, b_len, 1, 1}});
 }
 
+// Two arrays of int32 (NULL: none).
+bool ints_overlap(const int32_t* a, int64_t n_a, const int32_t* b, int64_t n_b) {
+  return a && b && overlap(a, b, 4, {{n_a, n_b, 1, 1}});
+}
+
 int attn(const pbs_tensor* Qt, const pbs_tensor* Kpt, const pbs_tensor* Vpt, bool prefix, const pbs_tensor* Kt,
          const pbs_tensor* Vt, const int32_t* kv_len, const int32_t* q_len, int64_t window, int n_sink,
          float softmax_scale, pbs_tensor* Ot, float* lse, void* ws, size_t ws_bytes, void* stream, const char* what) {
@@ -234,6 +239,10 @@ int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* Kt, cons
   if (overlap(p.Ko, p.K) || overlap(p.Ko, p.V) || overlap(p.Vo, p.K) || overlap(p.Vo, p.V) || overlap(p.Ko, p.Vo) ||
       rows_overlap(mass, mass_stride, p.K.N, mass_out, mass_out_stride, budget, p.K.B * p.K.H))
     return fail(PBS_ERR_INVALID_ARG, "outputs overlap inputs or each other");
+  const int64_t n_kept = p.K.B * p.K.H * budget;
+  if (ints_overlap(keep, n_kept, kv_len, p.K.B) || ints_overlap(keep, n_kept, new_len, p.K.B) ||
+      (new_len != kv_len && ints_overlap(new_len, p.K.B, kv_len, p.K.B)))
+    return fail(PBS_ERR_INVALID_ARG, "keep or new_len overlap kv_len or each other");
   if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::evict_ws_bytes(p.K))))) return rc;
   p.mass = mass;
   p.mass_stride = mass_stride;

@@ -62,10 +62,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   const float* mass = p.mass + row * p.mass_stride;
   int32_t* keep = p.keep + row * p.budget;
   const int n_keep = min(L, p.budget);
-  if (rank == 0) {
-    if (tid == 0 && p.new_len && row % p.K.H == 0) p.new_len[b] = n_keep;
+  if (rank == 0)
     for (int i = n_keep + tid; i < p.budget; i += kThreads) keep[i] = -1;
-  }
   if (L <= p.budget) {                             // (all of the cluster alike)
     for (int j = rank * kThreads + tid; j < L; j += kThreads * n_rank) keep[j] = j;
     return;
@@ -254,6 +252,10 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p) 
   wait_for_previous_kernel();
   const int blocks = (p.budget + RP * kGatherRows - 1) / (RP * kGatherRows);
   const int64_t row = blockIdx.x / blocks, b = row / p.K.H, h = row % p.K.H;
+  // (here, as new_len may be kv_len, which every CTA of the selection reads; nothing else
+  // reads it from here on)
+  if (p.new_len && h == 0 && blockIdx.x % blocks == 0 && threadIdx.x == 0)
+    p.new_len[b] = min(cache_len(p.kv_len, b, p.K.N, p.err), p.budget);
   const int c = threadIdx.x % CH * 8;
   const int i0 = static_cast<int>(blockIdx.x) % blocks * RP * kGatherRows + threadIdx.x / CH;
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.K.ptr) + b * p.K.sB + h * p.K.sH + c;

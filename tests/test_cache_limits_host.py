@@ -45,3 +45,17 @@ def test_workspace_of_refused_shapes(lib, op):
                  (desc(1, 4, 4), desc(1, 2, 300, D=128)), (desc(1 << 32, 1 << 32, 4), desc(1 << 32, 1 << 32, 300)),
                  (desc(300, 256, 1), desc(300, 256, 64)), (desc(64, 64, 1 << 30), desc(64, 1, 64))):
         assert lib.pbs_workspace_size(op, q, k, 0, 0) == 0
+
+
+def test_evict_refuses_overlapping_lengths(lib):
+    k, v = desc(3, 2, 256, ptr=0x1000000), desc(3, 2, 256, ptr=0x2000000)
+    ko, vo = desc(3, 2, 64, ptr=0x3000000), desc(3, 2, 64, ptr=0x4000000)
+
+    def call(kv_len, new_len, keep=0x30000):
+        return lib.pbs_evict(P(0x2000), 256, k, v, P(kv_len), 64, 8, 4, P(keep), P(new_len), ko, vo, P(0x50000), 64,
+                             None, 0, None)
+
+    end = 0x30000 + 4 * 3 * 2 * 64                          # of keep
+    for kv_len, new_len in ((0x9000, 0x9004), (0x9008, 0x9000), (0x30000, 0x9000), (end - 4, 0x9000),
+                            (0x9000, end - 4), (0x9000, 0x30000 - 8), (0, 0x30010)):
+        assert call(kv_len, new_len) == -1 and b"overlap" in lib.pbs_get_last_error(), (hex(kv_len), hex(new_len))

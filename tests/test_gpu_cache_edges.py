@@ -132,3 +132,22 @@ def test_infinite_values_of_both_signs():
     O, _ = pbs.pbs_attn_window(Q, K, V)
     assert torch.isnan(O[..., 5]).all() and (O[..., 6] == float("inf")).all()
     assert torch.isfinite(O[..., :5]).all() and torch.isfinite(O[..., 7:]).all()
+
+
+@pytest.mark.parametrize("B,Hkv,N,budget", [(3, 4, 900, 300), (1, 2, 70000, 5000), (2, 1, 140000, 3000), (5, 8, 64, 64)])
+def test_evict_with_lengths_in_place(B, Hkv, N, budget):
+    """One tensor of lengths goes in and comes out, with one CTA a row and with clusters."""
+    mass = torch.rand((B, Hkv, N), generator=torch.Generator(device="cuda").manual_seed(N), device="cuda")
+    K, V = inputs(11, B, 1, 1, 64, 1, N)[1:]
+    K, V = K.expand(B, Hkv, N, 64), V.expand(B, Hkv, N, 64)
+    start = torch.tensor([N - 7 * b if b != 1 else budget - 1 for b in range(B)], dtype=torch.int32, device="cuda")
+    want = pbs.pbs_evict(mass, K, V, budget, 20, 4, kv_len=start)
+    for _ in range(4):
+        n = start.clone()
+        got = pbs.pbs_evict(mass, K, V, budget, 20, 4, kv_len=n, new_len=n)
+        assert got[4] is n and n.tolist() == [min(int(x), budget) for x in start]
+        assert torch.equal(got[0], want[0])
+        for b in range(B):
+            m = int(n[b])
+            assert all(torch.equal(x[b, :, :m], y[b, :, :m]) for x, y in zip(got[1:4], want[1:4]))
+    pbs.pbs_check_device()
