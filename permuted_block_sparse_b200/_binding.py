@@ -562,7 +562,7 @@ def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int,
         else:
             _check_out("keep", keep, torch.int32, (B, Hkv, budget))
         if K_out is None:
-            K_out = K.new_empty((B, Hkv, budget, D))
+            K_out = K.new_empty((B, Hkv, budget if V_out is None else V_out.shape[2], D))
         if V_out is None:
             V_out = K.new_empty((B, Hkv, K_out.shape[2], D))
         if mass_out is None:

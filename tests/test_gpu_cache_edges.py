@@ -151,3 +151,15 @@ def test_evict_with_lengths_in_place(B, Hkv, N, budget):
             m = int(n[b])
             assert all(torch.equal(x[b, :, :m], y[b, :, :m]) for x, y in zip(got[1:4], want[1:4]))
     pbs.pbs_check_device()
+
+
+def test_evict_with_one_output_given():
+    """The other one gets its room."""
+    _, K, V = inputs(21, 2, 2, 2, 64, 1, 300)
+    mass = torch.rand((2, 2, 300), device="cuda")
+    want = pbs.pbs_evict(mass, K, V, 50)
+    for name in ("K_out", "V_out"):
+        room = torch.zeros((2, 2, 90, 64), dtype=torch.bfloat16, device="cuda")
+        _, Ko, Vo, _, _ = pbs.pbs_evict(mass, K, V, 50, **{name: room})
+        assert Ko.shape == Vo.shape == room.shape
+        assert torch.equal(Ko[:, :, :50], want[1]) and torch.equal(Vo[:, :, :50], want[2])
