@@ -59,3 +59,22 @@ def test_evict_refuses_overlapping_lengths(lib):
     for kv_len, new_len in ((0x9000, 0x9004), (0x9008, 0x9000), (0x30000, 0x9000), (end - 4, 0x9000),
                             (0x9000, end - 4), (0x9000, 0x30000 - 8), (0, 0x30010)):
         assert call(kv_len, new_len) == -1 and b"overlap" in lib.pbs_get_last_error(), (hex(kv_len), hex(new_len))
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_workspace_refusals(lib, op):
+    """Too small, misaligned and null, for shapes whose keys or rows are cut into parts."""
+    q, k = (desc(1, 4, 4000), desc(1, 1, 4000)) if op == pbs.PBS_OP_KEY_MASS else (desc(1, 4, 3), desc(1, 2, 1 << 20))
+    o = desc(q.B, q.H, q.N, ptr=0x80000000)
+    need = lib.pbs_workspace_size(op, q, k, 0, 0)
+    assert need > 0 and need % 256 == 0
+
+    def call(ws, n):
+        if op == pbs.PBS_OP_ATTN_WINDOW:
+            return lib.pbs_attn_window(q, k, k, None, None, 0, 0, 0.1, o, None, P(ws), n, None)
+        if op == pbs.PBS_OP_ATTN_PREFIX:
+            return lib.pbs_attn_prefix(q, k, k, k, k, None, None, 0.1, o, None, P(ws), n, None)
+        return lib.pbs_key_mass(q, k, P(0x2000), None, None, 0, 0, 1.0, 0.1, None, 0, P(0x90000000), k.N, P(ws), n, None)
+
+    for ws, n in ((0x4000, need - 1), (0x4000, 0), (0x4010, need), (0, need)):
+        assert call(ws, n) == -1 and b"workspace" in lib.pbs_get_last_error(), (hex(ws), n)
