@@ -404,7 +404,7 @@ int pbs_key_mass(const pbs_tensor* Q, const pbs_tensor* K, const float* lse, con
  *     with it as keys are appended).  None of them may overlap another, K, V
  *     or mass (views of one buffer that share no element are taken where
  *     their strides agree); K_out and V_out may not be broadcast views.
- *   ws: pbs_workspace_size(PBS_OP_EVICT, K, K, ...) bytes.                  */
+ *   ws: none is needed (pbs_workspace_size gives 0); it is not read.        */
 int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* K, const pbs_tensor* V,
               const int32_t* kv_len, int budget, int recent, int n_sink, int32_t* keep, int32_t* new_len,
               pbs_tensor* K_out, pbs_tensor* V_out, float* mass_out, int64_t mass_out_stride, void* ws,

@@ -547,7 +547,7 @@ def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int,
     last ``recent`` always stay and the rest are those of highest ``mass``.
     ``K_out`` and ``V_out`` [B, Hkv, n >= budget, D] and ``mass_out``
     [B, Hkv, n >= budget] take the kept rows at their start.  ``new_len`` may be
-    ``kv_len`` itself."""
+    ``kv_len`` itself.  No workspace is needed; ``ws`` is not read."""
     lib = _lib or load()
     k, v = describe(K), describe(V)
     B, Hkv, N, D = K.shape
@@ -574,9 +574,8 @@ def pbs_evict(mass: torch.Tensor, K: torch.Tensor, V: torch.Tensor, budget: int,
             new_len = K.new_empty((B,), dtype=torch.int32)
         else:
             _check_out("new_len", new_len, torch.int32, (B,))
-        ws, wp, wn = _cache_ws(ws, _cache_ws_bytes(PBS_OP_EVICT, B, Hkv, N, D, Hkv, N), K)
         rc = lib.pbs_evict(mass.data_ptr(), s_in, k, v, kv, budget, recent, n_sink, keep.data_ptr(),
-                           new_len.data_ptr(), describe(K_out), describe(V_out), mass_out.data_ptr(), s_out, wp, wn,
+                           new_len.data_ptr(), describe(K_out), describe(V_out), mass_out.data_ptr(), s_out, None, 0,
                            _raw_stream(K.get_device()))
     _check(rc)
     return keep, K_out, V_out, mass_out, new_len

@@ -238,7 +238,7 @@ size_t pbs_workspace_size(int op, const pbs_tensor* Qt, const pbs_tensor* Kt, in
       if (pbs::api_check_cache_shapes(Q, K)) return 0;
       return align256(pbs::key_mass_ws_bytes(Q, K));
     case PBS_OP_EVICT:
-      return align256(pbs::evict_ws_bytes(K));
+      return 0;
     default:
       break;
   }

@@ -216,8 +216,8 @@ int pbs_key_mass(const pbs_tensor* Qt, const pbs_tensor* Kt, const float* lse, c
 
 int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* Kt, const pbs_tensor* Vt,
               const int32_t* kv_len, int budget, int recent, int n_sink, int32_t* keep, int32_t* new_len,
-              pbs_tensor* Kot, pbs_tensor* Vot, float* mass_out, int64_t mass_out_stride, void* ws, size_t ws_bytes,
-              void* stream) {
+              pbs_tensor* Kot, pbs_tensor* Vot, float* mass_out, int64_t mass_out_stride, void* /*ws*/,
+              size_t /*ws_bytes*/, void* stream) {
   pbs::EvictParams p;
   int rc;
   if ((rc = pbs::api_check_tensor(Kt, "K", &p.K)) || (rc = pbs::api_check_tensor(Vt, "V", &p.V)) ||
@@ -243,7 +243,6 @@ int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* Kt, cons
   if (ints_overlap(keep, n_kept, kv_len, p.K.B) || ints_overlap(keep, n_kept, new_len, p.K.B) ||
       (new_len != kv_len && ints_overlap(new_len, p.K.B, kv_len, p.K.B)))
     return fail(PBS_ERR_INVALID_ARG, "keep or new_len overlap kv_len or each other");
-  if ((rc = pbs::api_check_ws(ws, ws_bytes, align256(pbs::evict_ws_bytes(p.K))))) return rc;
   p.mass = mass;
   p.mass_stride = mass_stride;
   p.mass_out_stride = mass_out_stride;
@@ -254,7 +253,6 @@ int pbs_evict(const float* mass, int64_t mass_stride, const pbs_tensor* Kt, cons
   p.keep = keep;
   p.new_len = new_len;
   p.mass_out = mass_out;
-  p.ws = ws;
   p.err = pbs::api_device_error_word();
   if (!p.err) return fail(PBS_ERR_CUDA, "cannot resolve the device error word");
   return launched(pbs::launch_evict(p, static_cast<cudaStream_t>(stream)), "evict");

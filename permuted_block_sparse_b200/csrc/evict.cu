@@ -287,8 +287,6 @@ __global__ void __launch_bounds__(256) evict_gather_kernel(const EvictParams p) 
 
 }  // namespace
 
-size_t evict_ws_bytes(const TensorDesc&) { return 0; }
-
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   const int64_t rows = p.K.B * p.K.H;
   const int per_cta = 256 / static_cast<int>(p.K.D / 8) * kGatherRows;

@@ -139,10 +139,8 @@ struct EvictParams {
   int32_t* keep;
   int32_t* new_len;       // NULL if not wanted
   float* mass_out;
-  void* ws;
   int* err;
 };
-size_t evict_ws_bytes(const TensorDesc& K);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 
 }  // namespace pbs
