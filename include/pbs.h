@@ -374,7 +374,13 @@ int pbs_attn_prefix(const pbs_tensor* Q, const pbs_tensor* Kp, const pbs_tensor*
  * for j < kv_len[b], and 0 for the others (a key appended later starts at
  * zero).
  *   lse: DEVICE fp32 [B, Hq, M], from whichever attention ran over these
- *     queries and keys; a row with lse = -inf adds nothing.
+ *     queries and keys; a row with lse = -inf adds nothing, and a row with
+ *     lse = NaN makes NaN of the keys that it sees.
+ *   After pbs_attn_prefix, K is the sequences' own cache, with the call's
+ *     kv_len and q_len.  Over Kp the rows here are causal: with M = 1 and Kp
+ *     broadcast over the sequences they see all of it, as there; with more
+ *     rows only the last one does, so pass each row as a sequence of its own
+ *     (Q as [B * M, Hq, 1, D], lse as [B * M, Hq, 1]).
  *   prev, mass: DEVICE fp32 [B, Hkv, N], successive (b, hkv) rows
  *     prev_stride / mass_stride elements apart (>= N).  prev may be NULL (no
  *     earlier mass; decay is not used) or the same buffer as mass.

@@ -515,7 +515,9 @@ def pbs_key_mass(Q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, mass: Opti
                  stream=None) -> torch.Tensor:
     """[B, Hkv, N] fp32: ``decay`` times the earlier ``mass`` (None: zero) plus
     the attention weight that the rows of ``Q`` give each key, from the ``lse``
-    of their attention.  ``out`` may be ``mass`` itself."""
+    of their attention.  ``out`` may be ``mass`` itself.  Rows are causal as in
+    :func:`pbs_attn_window`: for the mass of a shared prefix that every row sees
+    whole, pass each row as a sequence of its own over the broadcast prefix."""
     lib = _lib or load()
     q, k = describe(Q), describe(K)
     B, Hq, M, D = Q.shape

@@ -33,8 +33,14 @@
 // by 0 before the product and note the key; at the end each row that does see
 // such a key takes those entries from global memory.
 //
+// Roundings: statistics, sums and O in fp32; P to bf16 for its product, the only type
+// that goes with V (the row's sum is of P before the rounding).  Each weight is off by
+// 2^-8 at most, which leaves O 2.3e-3 from fp64 (2-norm) where the bf16 of O alone is
+// 1.65e-3; P as two bf16, as attn_few_kernel has it where HBM is the bound, would be
+// half as many products again where products are: 2.27 us a tile pair for 1.51.
+//
 // Bound: the tensor core; with few rows per CTA, HBM.  Measured (a 32K prompt, Hq 32,
-// Hkv 8, D 128, window 2048, 128 sinks): 1.29 ms, 875 TFLOP/s of visible products.
+// Hkv 8, D 128, window 2048, 128 sinks): 1.36 ms, 831 TFLOP/s of visible products.
 // One more tile for both slots costs 1.82 us, 1.60 with the softmax arithmetic left
 // out, 1.51 at the measured matrix rate; each CTA adds 13 us to its 18 tiles (set-up
 // and first loads 3.6, the two slots' ends 4.7, masked and cleaned tiles).  A

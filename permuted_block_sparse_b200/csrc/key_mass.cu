@@ -3,7 +3,9 @@
 // x_rj = scale log2(e) Q[r].K[j], y_r = log2(e) lse[r], over the query rows of
 // all heads of a KV head.  Products and exponentials in fp32; the weights of up
 // to 128 rows are added in fp32, those sums in fp64 (a prompt adds tens of
-// thousands of small terms to one key), or in fp32 where there are at most eight.
+// thousands of small terms to one key), or in fp32 where there are at most eight: in
+// launches of two, with the mass so far rounded to fp32 after each, which for weights
+// that are never negative is 2^-24 of the result a launch.
 // No atomics: a key's sum has one owner, or parts that a second kernel adds in order.
 //
 // The keys are the rows of the MMA in all kernels (S^T = K Q^T), so that a
@@ -61,7 +63,7 @@ __device__ __forceinline__ uint32_t columns_in(int c, int c_lo, int c_hi) {
 // as the B operand.  Groups that no row sees (outside a window) are not among them:
 // their mass is carried over beside the first loads.  The CTAs take groups in turn.
 // Bound: HBM, 2 D bytes per visible key.  Measured: 32 sequences of 4096 to 8192 keys
-// (Hq 32, Hkv 8, D 128) 66 us, 6.4 TB/s; 200 rows of 30000 keys under a window of 1000
+// (Hq 32, Hkv 8, D 128) 65 us, 6.4 TB/s; 200 rows of 30000 keys under a window of 1000
 // 33 us (88 with the unseen groups in the loop).
 // Sixteen warps per SM (four CTAs of 48 KB) hide the chain from a group's arrival
 // to its sums; with eight the schedulers issued in 41% of the cycles.
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFewCtas) mass_few_kernel(const K
 //   warps 2-17 copy K into tensor memory, then take 2^(x - y) of every column and
 //     sum it: a thread has one key and 64 of the 128 columns.
 // Bound: exponentials, 16 per clock and SM on the SFU.  Measured: a prompt of 8192
-// (Hq 32, Hkv 8, D 128) 347 us, 3.1 T weights/s, of which the SFU needs 231; the
+// (Hq 32, Hkv 8, D 128) 344 us, 3.1 T weights/s, of which the SFU needs 231; the
 // products and hand-offs alone take 288.  A ring of four buffers with K in shared
 // memory takes 396, products of 64 columns 458.
 constexpr int kWideThreads = 576;

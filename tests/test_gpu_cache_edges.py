@@ -4,7 +4,7 @@ import torch
 
 import cache_util as cu
 import permuted_block_sparse_b200 as pbs
-from test_gpu_cache import inputs
+from test_gpu_cache import inputs, lens
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +163,26 @@ def test_evict_with_one_output_given():
         _, Ko, Vo, _, _ = pbs.pbs_evict(mass, K, V, 50, **{name: room})
         assert Ko.shape == Vo.shape == room.shape
         assert torch.equal(Ko[:, :, :50], want[1]) and torch.equal(Vo[:, :, :50], want[2])
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_mass_of_a_shared_prefix(M):
+    """Each row as a sequence of its own over the broadcast prefix, and the own keys as
+    they lie: what all rows give in all is one per row and head.  A logit of 64 products
+    is off by 64 2^-24 of its absolute sum, which is below 8 here, and the LSE by as
+    much: 2^-14 of a weight in all."""
+    B, Hq, Hkv, d, P, N = 3, 8, 2, 64, 300, 90
+    Q, K, V = inputs(31, B, Hq, Hkv, d, M, N)
+    _, Kp, Vp = inputs(41, 1, Hkv, Hkv, d, 1, P)
+    kv = lens([90, 3, 40])
+    _, lse = pbs.pbs_attn_prefix(Q, Kp, Vp, K, V, kv_len=kv)
+    rows, rows_lse = Q.transpose(1, 2).reshape(B * M, Hq, 1, d), lse.transpose(1, 2).reshape(B * M, Hq, 1)
+    shared = pbs.pbs_key_mass(rows, Kp.expand(B * M, -1, -1, -1), rows_lse)
+    own = pbs.pbs_key_mass(Q, K, lse, kv_len=kv)
+    pbs.pbs_check_device()
+    want = torch.exp(rows.double() @ Kp.double().repeat_interleave(Hq // Hkv, 1).transpose(2, 3) * d ** -0.5
+                     - rows_lse.double()[..., None])
+    want = want.reshape(B * M, Hkv, Hq // Hkv, P).sum(2)
+    assert (shared.double() - want).abs().max() <= 2.0 ** -14 * float(want.max())
+    total = shared.reshape(B, M, -1).sum((1, 2)) + own.sum((1, 2))
+    assert (total - M * Hq).abs().max() <= 2.0 ** -12 * M * Hq
